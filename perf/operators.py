@@ -12,7 +12,7 @@ the values.  Types: "bf16"; "mxfp8" (E4M3 elements) and "mxfp4" (E2M1 elements, 
 2j in the low nibble), both with one E8M0 scale for 32 neighbouring elements of a row.
 
 Quantisation of a block x[0..31] (a = max |x|):
-  e = the smallest integer with a <= m * 2^e, clamped to [-117, c]    (mxfp8: m = 448, c = 7; mxfp4: m = 6, c = 13)
+  e = the smallest integer with a <= m * 2^e, clamped to [-100, c]    (mxfp8: m = 448, c = 7; mxfp4: m = 6, c = 13)
   element = x * 2^-e rounded to the element type, to nearest, ties to even, limited to +-m; scale code = e + 127
 A cached element stands for element * 2^e, which BF16 holds exactly.
 
@@ -141,7 +141,7 @@ def _quantise(x, kv):
     b = x.unflatten(-1, (-1, 32))
     m, ex = torch.frexp(b.abs().amax(-1))
     mt, et = math.frexp(top)
-    e = torch.where(m > mt, ex - et + 1, ex - et).clamp(-117, cap)
+    e = torch.where(m > mt, ex - et + 1, ex - et).clamp(-100, cap)
     y = torch.ldexp(b, -e.unsqueeze(-1)).clamp(-top, top)
     if kv == "mxfp8":
         code = y.to(torch.float8_e4m3fn).view(torch.uint8).flatten(-2)
@@ -326,7 +326,7 @@ def _rounded(x, kv):
     e = torch.floor(torch.log2(torch.where(a > 0, a, 1.0) / top))
     e = torch.where(a > top * torch.exp2(e), e + 1, e)  # the smallest e with a <= top * 2^e
     e = torch.where(a <= top * torch.exp2(e - 1), e - 1, e)
-    e = torch.where(a > 0, e, -117.0).clamp(-117, cap)
+    e = torch.where(a > 0, e, -100.0).clamp(-100, cap)
     y = (b * torch.exp2(-e)).clamp(-top, top)
     low, bits = (-6, 3) if kv == "mxfp8" else (0, 1)
     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** low))) - bits)
