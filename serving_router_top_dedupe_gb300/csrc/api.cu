@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "ft_internal.cuh"
+#include "ft_kv_internal.cuh"
 #include "ft_prefill.cuh"
 
 namespace {
@@ -37,6 +38,21 @@ ft_status fail(ft_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+
+}  // namespace
+
+namespace ft {
+ft_status kv_fail(ft_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+}  // namespace ft
+
+namespace {
 
 // Memory of ft_host_alloc: the registered address -> its mapping (base NULL: cudaHostAlloc).
 struct HostMap {

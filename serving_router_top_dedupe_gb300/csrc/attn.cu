@@ -1,0 +1,121 @@
+// ft_attn: argument checks, workspace and the choice of the kernel.
+#include <cmath>
+
+#include "ft_kv_internal.cuh"
+
+namespace ft {
+namespace kv {
+
+cudaError_t attn_rows_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_rows_mxfp8(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_rows_mxfp4(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device (0: the query failed), looked up once per device.
+int sm_count() {
+  static int cache[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = __atomic_load_n(&cache[dev], __ATOMIC_RELAXED);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    __atomic_store_n(&cache[dev], n, __ATOMIC_RELAXED);
+  }
+  return n;
+}
+
+// Counters, and two partial results for each CTA: 16 rows of head_dim + 2 floats, two CTAs per SM.
+size_t workspace_need(int n_sm, int D) { return kCounterBytes + (size_t)n_sm * 2 * 2 * 16 * (D + 2) * 4; }
+
+ft_status check_heads(const char* name, int n_heads, int n_kv_heads, int head_dim) {
+  if (n_kv_heads < 1 || n_kv_heads > 1024 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128)
+    return kv_fail(FT_ERR_INVALID, "%s: n_heads = %d over %d cache heads", name, n_heads, n_kv_heads);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return kv_fail(FT_ERR_INVALID, "%s: head_dim = %d (64, 128 or 256)", name, head_dim);
+  return FT_OK;
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace ft
+
+using namespace ft;
+
+extern "C" ft_status ft_attn_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes_out) {
+  if (!bytes_out) return kv_fail(FT_ERR_INVALID, "ft_attn_workspace: bytes_out is NULL");
+  if (ft_status st = kv::check_heads("ft_attn_workspace", n_heads, n_kv_heads, head_dim)) return st;
+  const int n_sm = kv::sm_count();
+  if (!n_sm) return kv_fail(FT_ERR_CUDA, "ft_attn_workspace: no device");
+  *bytes_out = kv::workspace_need(n_sm, head_dim);
+  return FT_OK;
+}
+
+extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* stream) {
+  const char* name = "ft_attn";
+  if (ft_status st = kv::check_cache(name, c)) return st;
+  if (!a) return kv_fail(FT_ERR_INVALID, "%s: args is NULL", name);
+  if (ft_status st = kv::check_heads(name, a->n_heads, c->n_kv_heads, c->head_dim)) return st;
+  if (a->n_tokens < 0 || a->n_seqs < 0 || a->n_seqs > kv::kMaxSeqs || a->max_new < 1 ||
+      (long long)a->n_tokens * a->n_heads >= (1ll << 31))
+    return kv_fail(FT_ERR_INVALID, "%s: n_tokens = %d, n_seqs = %d, max_new = %d", name, a->n_tokens, a->n_seqs,
+                   a->max_new);
+  if (a->table_stride < 1 || (long long)a->table_stride * c->page_size > (1ll << 30) || a->window < 0 ||
+      (a->causal != 0 && a->causal != 1) || !std::isfinite(a->scale))
+    return kv_fail(FT_ERR_INVALID, "%s: table_stride = %d, window = %d, causal = %d, scale = %g", name,
+                   a->table_stride, a->window, a->causal, (double)a->scale);
+  if (a->n_tokens == 0 || a->n_seqs == 0) return FT_OK;
+  if (!a->q || !a->q_start || !a->kv_len || !a->page_table || !a->out || !a->workspace)
+    return kv_fail(FT_ERR_INVALID, "%s: a pointer is NULL", name);
+  const uintptr_t b16 = reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out);
+  const uintptr_t b4 = reinterpret_cast<uintptr_t>(a->q_start) | reinterpret_cast<uintptr_t>(a->kv_len) |
+                       reinterpret_cast<uintptr_t>(a->page_table) | reinterpret_cast<uintptr_t>(a->lse) |
+                       reinterpret_cast<uintptr_t>(a->error_word_out);
+  if ((b16 & 15) || (b4 & 3) || (reinterpret_cast<uintptr_t>(a->workspace) & 255))
+    return kv_fail(FT_ERR_INVALID, "%s: q and out must be 16-byte, the workspace 256-byte aligned", name);
+  const long long width = (long long)a->n_heads * c->head_dim;
+  if (a->q_stride % 8 || a->out_stride % 8 || a->q_stride < 0 || (a->n_tokens > 1 && a->out_stride < width))
+    return kv_fail(FT_ERR_INVALID, "%s: strides %lld, %lld (multiples of 8; rows of out must not overlap)", name,
+                   a->q_stride, a->out_stride);
+  const int n_sm = kv::sm_count();
+  if (!n_sm) return kv_fail(FT_ERR_CUDA, "%s: no device", name);
+  if (a->workspace_bytes < kv::workspace_need(n_sm, c->head_dim))
+    return kv_fail(FT_ERR_CAPACITY, "%s: the workspace has %zu bytes, %zu are needed", name, a->workspace_bytes,
+                   kv::workspace_need(n_sm, c->head_dim));
+
+  kv::AttnParams p{};
+  p.k = static_cast<const uint8_t*>(c->k);
+  p.v = static_cast<const uint8_t*>(c->v);
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.n_pages = c->n_pages;
+  p.page_size = c->page_size;
+  p.page_shift = kv::page_shift(c->page_size);
+  p.n_kv_heads = c->n_kv_heads;
+  p.n_heads = a->n_heads;
+  p.group = a->n_heads / c->n_kv_heads;
+  p.n_tokens = a->n_tokens;
+  p.n_seqs = a->n_seqs;
+  p.table_stride = a->table_stride;
+  p.causal = a->causal;
+  p.window = a->window < (1 << 30) ? a->window : 1 << 30;
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634074);
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_stride = a->q_stride;
+  p.q_start = a->q_start;
+  p.kv_len = a->kv_len;
+  p.page_table = a->page_table;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.out_stride = a->out_stride;
+  p.lse = a->lse;
+  p.counters = static_cast<uint32_t*>(a->workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kv::kCounterBytes);
+  p.error_word = a->error_word_out;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = c->kv_type == FT_KV_BF16    ? kv::attn_rows_bf16(p, c->head_dim, n_sm, s)
+                        : c->kv_type == FT_KV_MXFP8 ? kv::attn_rows_mxfp8(p, c->head_dim, n_sm, s)
+                                                    : kv::attn_rows_mxfp4(p, c->head_dim, n_sm, s);
+  return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+}

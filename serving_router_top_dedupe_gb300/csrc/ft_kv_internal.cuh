@@ -1,0 +1,263 @@
+// Shared pieces of the paged key/value cache: the formats' decoding, the swizzled layout of
+// rows in shared memory, and how ft_attn's work is cut and joined again.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ft_internal.cuh"
+#include "ft_kv.h"
+
+namespace ft {
+
+// Sets ft_last_error() of this thread (api.cu) and returns s.
+ft_status kv_fail(ft_status s, const char* fmt, ...);
+
+namespace kv {
+
+// Bytes of one cached row's elements, and of its scales.
+__host__ __device__ constexpr int row_bytes(int type, int D) {
+  return type == FT_KV_BF16 ? 2 * D : type == FT_KV_MXFP8 ? D : D / 2;
+}
+__host__ __device__ constexpr int scale_bytes(int type, int D) { return type == FT_KV_BF16 ? 0 : D / 32; }
+
+// What decoded MXFP4 elements are still to be multiplied with: their codes become BF16 numbers
+// with an exponent 126 too small, and one BF16 multiplier cannot hold 2^126 * 2^e for every
+// scale, so 2^-16 is left in (the attention takes it out of its scores and sums in FP32).
+__host__ __device__ constexpr float left_in(int type) { return type == FT_KV_MXFP4 ? 65536.f : 1.f; }
+
+inline int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
+// Argument checks of a cache description (kv_cache.cu).
+ft_status check_cache(const char* name, const ft_kv_cache* c);
+
+// --------------------------------------------------------------------------- attention
+
+struct AttnParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  int n_pages, page_size, page_shift, n_kv_heads;
+  int n_heads, group;  // group = n_heads / n_kv_heads
+  int n_tokens, n_seqs, table_stride, causal, window;
+  float scale_log2;  // scale * log2(e)
+  const uint16_t* q;
+  long long q_stride;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  uint16_t* out;
+  long long out_stride;
+  float* lse;
+  uint32_t* counters;  // [kMaxCtas], zero between calls
+  float* partials;
+  uint32_t* error_word;
+};
+
+constexpr int kMaxCtas = 4096;                     // CTAs of one attention launch, at most
+constexpr size_t kCounterBytes = kMaxCtas * 4;
+constexpr int kMaxSeqs = 1024;                     // sequences of one call
+
+// How the work is cut.  The rows of one cache head of a sequence (row r: new token r / group,
+// query head r % group of the head's group) form blocks of RB rows.  An item is a block of
+// one head over the tiles (UT cached tokens) that its rows may see; items are ordered by
+// sequence, block and head, and every CTA takes the same number of consecutive tiles.  So
+// every CTA has the same work whatever the lengths, an item whose tiles fall to several CTAs
+// leaves one partial result in each (sums without their normalisation, and the maximum they
+// refer to), and the CTA that finishes last joins them in order.  Each CTA has at most two
+// such items, one that began before it (partial slot 2 * cta) and one that goes on after it
+// (2 * cta + 1).
+struct Cursor {
+  int seq, rb, head;
+  int q0, n, len, nb;  // of the sequence: first row of q, new tokens, cached length, row blocks
+  int lo, hi;          // cached tokens that any row of the block may see
+  int t0, cost;        // the block's first tile, and its tiles (at least 1)
+  long long start;     // position of the item's first tile in the order of all tiles
+};
+
+__device__ __forceinline__ void seq_range(const AttnParams& p, int s, int& q0, int& n, int& len, bool& bad) {
+  const int a = __ldg(p.q_start + s), b = __ldg(p.q_start + s + 1), l = __ldg(p.kv_len + s);
+  const int cap = p.table_stride << p.page_shift;
+  q0 = min(max(a, 0), p.n_tokens);
+  n = max(min(max(b, 0), p.n_tokens) - q0, 0);
+  len = min(max(l, 0), cap);
+  bad = a != q0 || b < a || b > p.n_tokens || l != len;
+}
+
+// Row blocks of a sequence with n new tokens.
+template <int RB>
+__device__ __forceinline__ int row_blocks(int n, int group) {
+  return (int)(((long long)n * group + RB - 1) / RB);
+}
+
+// The cached tokens that rows [rb * RB, ...) of the sequence may see, in tiles of UT tokens.
+template <int RB, int UT>
+__device__ __forceinline__ void block_range(const AttnParams& p, int rb, int n, int len, int& lo, int& hi, int& t0,
+                                            int& cost) {
+  const int rows = n * p.group, r0 = rb * RB, r1 = min(rows, r0 + RB) - 1;
+  const int p0 = len - n + r0 / p.group, p1 = len - n + r1 / p.group;
+  hi = p.causal ? min(len, p1 + 1) : len;
+  hi = max(hi, 0);
+  lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), hi) : 0;
+  t0 = lo / UT;
+  cost = max((hi + UT - 1) / UT - t0, 1);
+}
+
+template <int RB, int UT>
+__device__ __forceinline__ void cursor_seq(const AttnParams& p, Cursor& c) {
+  bool bad;
+  seq_range(p, c.seq, c.q0, c.n, c.len, bad);
+  c.nb = row_blocks<RB>(c.n, p.group);
+}
+
+// To the next item (the caller knows that there is one).
+template <int RB, int UT>
+__device__ __forceinline__ void cursor_next(const AttnParams& p, Cursor& c) {
+  c.start += c.cost;
+  if (++c.head < p.n_kv_heads) return;
+  c.head = 0;
+  if (++c.rb == c.nb) {
+    c.rb = 0;
+    do {
+      ++c.seq;
+      cursor_seq<RB, UT>(p, c);
+    } while (c.nb == 0 && c.seq + 1 < p.n_seqs);
+  }
+  block_range<RB, UT>(p, c.rb, c.n, c.len, c.lo, c.hi, c.t0, c.cost);
+}
+
+struct PlanSmem {
+  long long sum[kMaxSeqs];  // tiles of a sequence's blocks (one head), then their prefix sums
+  long long part[32];
+  Cursor cur;
+  long long total;
+  int found;
+};
+
+// All NT threads of the block (a multiple of 32): the number of tiles per CTA, and the item
+// that contains the CTA's first tile.  Returns false for a CTA without work.  Costs are
+// counted per head and multiplied at the end.
+template <int RB, int UT, int NT>
+__device__ bool plan(const AttnParams& p, PlanSmem& sm, Cursor& cur, long long& w0, long long& w1, long long& per) {
+  constexpr int kFew = 4;  // blocks of a sequence that one thread counts
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool any_bad = false;
+  int many = 0;
+  for (int s = tid; s < p.n_seqs; s += NT) {
+    int q0, n, len;
+    bool bad;
+    seq_range(p, s, q0, n, len, bad);
+    any_bad |= bad;
+    const int nb = row_blocks<RB>(n, p.group);
+    long long sum = 0;
+    if (nb <= kFew) {
+      for (int b = 0; b < nb; ++b) {
+        int lo, hi, t0, cost;
+        block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
+        sum += cost;
+      }
+    } else {
+      sum = -1;
+      many = 1;
+    }
+    sm.sum[s] = sum;
+  }
+  if (any_bad && blockIdx.x == 0 && p.error_word) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+  if (tid == 0) sm.found = -1;
+  many = __syncthreads_or(many);
+  // sequences of many blocks: a warp counts each
+  if (many) {
+    for (int s = warp; s < p.n_seqs; s += NT / 32) {
+      if (sm.sum[s] >= 0) continue;
+      int q0, n, len;
+      bool bad;
+      seq_range(p, s, q0, n, len, bad);
+      const int nb = row_blocks<RB>(n, p.group);
+      long long sum = 0;
+      for (int b = lane; b < nb; b += 32) {
+        int lo, hi, t0, cost;
+        block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
+        sum += cost;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncwarp();
+      if (lane == 0) sm.sum[s] = sum;
+    }
+    __syncthreads();
+  }
+  // prefix sums over the sequences (warp 0, 32 at a time)
+  if (warp == 0) {
+    long long run = 0;
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+      const int s = s0 + lane;
+      const long long v = s < p.n_seqs ? sm.sum[s] : 0;
+      long long x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (s < p.n_seqs) sm.sum[s] = run + x - v;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) sm.total = run * p.n_kv_heads;
+  }
+  __syncthreads();
+  const long long total = sm.total;
+  per = (total + gridDim.x - 1) / gridDim.x;
+  w0 = per * blockIdx.x;
+  w1 = min(w0 + per, total);
+  if (w0 >= w1) return false;
+  // the sequence: the last one that begins at or before w0 and has any tiles
+  const long long at = w0 / p.n_kv_heads;  // in tiles of one head: inside the same block
+  for (int s = tid; s < p.n_seqs; s += NT) {
+    const long long a = sm.sum[s], b = s + 1 < p.n_seqs ? sm.sum[s + 1] : total / p.n_kv_heads;
+    if (a <= at && at < b) sm.found = s;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Cursor c{};
+    c.seq = sm.found;
+    cursor_seq<RB, UT>(p, c);
+    long long run = sm.sum[c.seq];
+    for (int b0 = 0; b0 < c.nb; b0 += 32) {
+      int lo = 0, hi = 0, t0 = 0, cost = 0;
+      if (b0 + lane < c.nb) block_range<RB, UT>(p, b0 + lane, c.n, c.len, lo, hi, t0, cost);
+      int x = cost;  // 32 blocks of at most 2^31 / UT tiles
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const bool here = cost > 0 && at < run + x && at >= run + x - cost;
+      if (here) {
+        c.rb = b0 + lane;
+        c.lo = lo;
+        c.hi = hi;
+        c.t0 = t0;
+        c.cost = cost;
+        const long long first = (run + x - cost) * p.n_kv_heads;  // the block's first head
+        c.head = (int)((w0 - first) / cost);
+        c.start = first + (long long)c.head * cost;
+        sm.cur = c;
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  cur = sm.cur;
+  return true;
+}
+
+// Pieces of the item at `cur`: the CTAs that hold its first and its last tile.
+__device__ __forceinline__ void piece_owners(const Cursor& cur, long long per, int& first, int& last) {
+  first = (int)(cur.start / per);
+  last = (int)((cur.start + cur.cost - 1) / per);
+}
+
+}  // namespace kv
+}  // namespace ft

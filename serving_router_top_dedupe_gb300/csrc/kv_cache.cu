@@ -1,0 +1,275 @@
+// Paged key/value cache: writing new tokens' rows (quantised on the way) and gathering cached
+// rows, plus the argument checks of the cache's entry points.
+//
+// Both kernels move each byte once and compute next to nothing, so memory bounds them.  One
+// thread takes one 1x32 block (BF16 input 64 bytes, in four 16-byte loads), which makes the
+// block's maximum a matter of one thread and its stores 32 or 16 bytes wide; a block's
+// neighbours in a warp are its row's, so a warp's accesses cover whole rows.
+#include <cstdarg>
+#include <cstdio>
+
+#include "ft_dot.cuh"
+#include "ft_kv_internal.cuh"
+
+namespace ft {
+namespace kv {
+
+ft_status check_cache(const char* name, const ft_kv_cache* c) {
+  if (!c) return kv_fail(FT_ERR_INVALID, "%s: cache is NULL", name);
+  if (c->kv_type != FT_KV_BF16 && c->kv_type != FT_KV_MXFP8 && c->kv_type != FT_KV_MXFP4)
+    return kv_fail(FT_ERR_INVALID, "%s: kv_type = %d", name, c->kv_type);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return kv_fail(FT_ERR_INVALID, "%s: head_dim = %d (64, 128 or 256)", name, c->head_dim);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return kv_fail(FT_ERR_INVALID, "%s: page_size = %d (16, 32, 64 or 128)", name, c->page_size);
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->n_pages < 1 ||
+      (long long)c->n_pages * c->n_kv_heads * c->page_size >= (1ll << 31))
+    return kv_fail(FT_ERR_INVALID, "%s: n_kv_heads = %d, n_pages = %d", name, c->n_kv_heads, c->n_pages);
+  const bool q = c->kv_type != FT_KV_BF16;
+  if (!c->k || !c->v || (q && (!c->k_scale || !c->v_scale)))
+    return kv_fail(FT_ERR_INVALID, "%s: a pointer of the cache is NULL", name);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v) |
+                         (q ? reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) : 0);
+  if (bits & 15) return kv_fail(FT_ERR_INVALID, "%s: the cache must be 16-byte aligned", name);
+  return FT_OK;
+}
+
+namespace {
+
+constexpr int kThreads = 128;
+
+struct RowsParams {
+  uint8_t *k, *v, *ks, *vs;
+  const uint16_t *k_in, *v_in;
+  uint16_t *k_out, *v_out;
+  long long k_stride, v_stride;
+  const int32_t* slots;
+  int n_tokens, n_kv_heads, page_size, page_shift, n_slots;
+  uint32_t* error_word;
+};
+
+// Scale exponent of a block whose largest magnitude has the FP32 bits `a`: the smallest e with
+// value <= m * 2^e, by comparing significands (m = 1.75 * 2^8 or 1.5 * 2^2).
+template <int TYPE>
+__device__ __forceinline__ int block_exponent(uint32_t a) {
+  constexpr uint32_t top = TYPE == FT_KV_MXFP8 ? 0x600000u : 0x400000u;  // fraction bits of m
+  constexpr int em = TYPE == FT_KV_MXFP8 ? 8 : 2, cap = TYPE == FT_KV_MXFP8 ? 7 : 13;
+  const int e = (int)(a >> 23) - 127 - em + ((a & 0x7fffffu) > top ? 1 : 0);
+  return min(max(e, -100), cap);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e2m1x8(const float* f) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+
+// Block of 32 BF16 values -> 32 or 16 bytes of codes and the scale code.
+template <int TYPE>
+__device__ __forceinline__ uint8_t quantise(const uint4* in, uint4* codes) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[4 * i] = in[i].x;
+    w[4 * i + 1] = in[i].y;
+    w[4 * i + 2] = in[i].z;
+    w[4 * i + 3] = in[i].w;
+  }
+  uint32_t top = 0;  // of the magnitudes, as 16-bit patterns in both halves
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  const uint32_t a = max(top >> 16, top & 0xffffu) << 16;
+  const bool nan = a >= 0x7f800000u;  // a NaN or an infinity: the whole block reads back as NaN
+  const int e = block_exponent<TYPE>(a);
+  const float inv = nan ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
+  }
+  uint32_t c[8];
+  if (TYPE == FT_KV_MXFP8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = nan ? 0u : e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    codes[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = nan ? 0u : e2m1x8(f + 8 * i);
+  }
+  codes[0] = make_uint4(c[0], c[1], c[2], c[3]);
+  return nan ? 255 : (uint8_t)(e + 127);
+}
+
+// What a block's codes and scale stand for, as 32 BF16 values.
+template <int TYPE>
+__device__ __forceinline__ void stands_for(const uint4* codes, uint32_t scale, uint4* out) {
+  // 2^e in FP32; code 255 is infinity here, and a NaN block's codes are zero: 0 * inf is NaN
+  const float s = __uint_as_float(scale << 23);
+  const uint32_t in[8] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w,
+                          TYPE == FT_KV_MXFP8 ? codes[1].x : 0, TYPE == FT_KV_MXFP8 ? codes[1].y : 0,
+                          TYPE == FT_KV_MXFP8 ? codes[1].z : 0, TYPE == FT_KV_MXFP8 ? codes[1].w : 0};
+  uint32_t o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float2 f;
+    if (TYPE == FT_KV_MXFP8) {
+      f = dot::e4m3x2_to_float2((uint16_t)(in[i / 2] >> (16 * (i & 1))));
+    } else {
+      const uint32_t h2 = dot::e2m1x2_to_f16x2((in[i / 4] >> (8 * (i & 3))) & 0xffu);
+      f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    }
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);  // exact
+    o[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
+// Slot of token t: >= 0, or -1 for a row that is not there.
+__device__ __forceinline__ int slot_of(const RowsParams& p, int t) {
+  const int s = __ldg(p.slots + t);
+  if (s < p.n_slots) return s < 0 ? -1 : s;
+  if (p.error_word) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+  return -1;
+}
+
+// Thread = one block of 32 elements of a row of K (blockIdx.y 0) or V (1).
+template <int TYPE, int D, bool WRITE>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
+  constexpr int NB = D / 32;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const int per = p.n_kv_heads * NB;
+  const int t = (int)(i / per);
+  if (t >= p.n_tokens) return;
+  const int r = (int)(i - (long long)t * per), head = r / NB, b = r % NB;
+  const bool is_v = blockIdx.y != 0;
+  const int slot = slot_of(p, t);
+  const long long dense = (long long)t * (is_v ? p.v_stride : p.k_stride) + head * D + b * 32;
+  const long long row = (((long long)(slot >> p.page_shift) * p.n_kv_heads + head) << p.page_shift) +
+                        (slot & (p.page_size - 1));
+  uint4* codes = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + row * row_bytes(TYPE, D) + b * row_bytes(TYPE, 32));
+  uint8_t* scale = TYPE == FT_KV_BF16 ? nullptr : (is_v ? p.vs : p.ks) + row * NB + b;
+  uint4 x[4];
+  if (WRITE) {
+    if (slot < 0) return;
+    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_in : p.k_in) + dense);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __ldg(src + j);
+    if constexpr (TYPE == FT_KV_BF16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) codes[j] = x[j];
+    } else {
+      uint4 c[2];
+      *scale = quantise<TYPE>(x, c);
+      codes[0] = c[0];
+      if (TYPE == FT_KV_MXFP8) codes[1] = c[1];
+    }
+  } else {
+    if (slot < 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = make_uint4(0, 0, 0, 0);
+    } else if constexpr (TYPE == FT_KV_BF16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = codes[j];
+    } else {
+      uint4 c[2];
+      c[0] = codes[0];
+      if (TYPE == FT_KV_MXFP8) c[1] = codes[1];
+      stands_for<TYPE>(c, *scale, x);
+    }
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + dense);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[j] = x[j];
+  }
+}
+
+template <int TYPE, int D>
+void launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
+  const long long threads = (long long)p.n_tokens * p.n_kv_heads * (D / 32);
+  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
+  if (write) rows_kernel<TYPE, D, true><<<grid, kThreads, 0, s>>>(p);
+  else rows_kernel<TYPE, D, false><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <int TYPE>
+void launch_rows_d(int D, const RowsParams& p, bool write, cudaStream_t s) {
+  if (D == 64) launch_rows_t<TYPE, 64>(p, write, s);
+  else if (D == 128) launch_rows_t<TYPE, 128>(p, write, s);
+  else launch_rows_t<TYPE, 256>(p, write, s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+ft_status rows_call(const char* name, const ft_kv_cache* c, int n_tokens, const void* k, const void* v,
+                    long long k_stride, long long v_stride, const int32_t* slots, uint32_t* error_word, bool write,
+                    void* stream) {
+  if (ft_status st = check_cache(name, c)) return st;
+  if (n_tokens < 0) return kv_fail(FT_ERR_INVALID, "%s: n_tokens = %d", name, n_tokens);
+  if (n_tokens == 0) return FT_OK;
+  if (!k || !v || !slots) return kv_fail(FT_ERR_INVALID, "%s: a pointer is NULL", name);
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 3))
+    return kv_fail(FT_ERR_INVALID, "%s: rows must be 16-byte aligned, slots 4-byte aligned", name);
+  const long long width = (long long)c->n_kv_heads * c->head_dim;
+  const bool bad = k_stride % 8 || v_stride % 8 || k_stride < 0 || v_stride < 0;
+  if (bad || (!write && n_tokens > 1 && (k_stride < width || v_stride < width)))
+    return kv_fail(FT_ERR_INVALID, "%s: strides %lld, %lld (multiples of 8; rows written must not overlap)", name,
+                   k_stride, v_stride);
+  RowsParams p{};
+  p.k = static_cast<uint8_t*>(c->k);
+  p.v = static_cast<uint8_t*>(c->v);
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.k_in = p.k_out = const_cast<uint16_t*>(static_cast<const uint16_t*>(k));
+  p.v_in = p.v_out = const_cast<uint16_t*>(static_cast<const uint16_t*>(v));
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.n_tokens = n_tokens;
+  p.n_kv_heads = c->n_kv_heads;
+  p.page_size = c->page_size;
+  p.page_shift = page_shift(c->page_size);
+  p.n_slots = c->n_pages * c->page_size;
+  p.error_word = error_word;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->kv_type == FT_KV_BF16) launch_rows_d<FT_KV_BF16>(c->head_dim, p, write, s);
+  else if (c->kv_type == FT_KV_MXFP8) launch_rows_d<FT_KV_MXFP8>(c->head_dim, p, write, s);
+  else launch_rows_d<FT_KV_MXFP4>(c->head_dim, p, write, s);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace ft
+
+extern "C" ft_status ft_kv_write(const ft_kv_cache* cache, int n_tokens, const void* k_bf16, const void* v_bf16,
+                                 long long k_stride, long long v_stride, const int32_t* slots,
+                                 uint32_t* error_word_out, void* stream) {
+  return ft::kv::rows_call("ft_kv_write", cache, n_tokens, k_bf16, v_bf16, k_stride, v_stride, slots, error_word_out,
+                           true, stream);
+}
+
+extern "C" ft_status ft_kv_read(const ft_kv_cache* cache, int n_tokens, const int32_t* slots, void* k_out, void* v_out,
+                                long long k_stride, long long v_stride, uint32_t* error_word_out, void* stream) {
+  return ft::kv::rows_call("ft_kv_read", cache, n_tokens, k_out, v_out, k_stride, v_stride, slots, error_word_out,
+                           false, stream);
+}

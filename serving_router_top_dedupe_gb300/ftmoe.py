@@ -26,6 +26,8 @@ FT_DEVERR_NAN_LOGIT, FT_DEVERR_BAD_STATE, FT_DEVERR_TIMEOUT, FT_DEVERR_CAPACITY 
 FT_TEST_HANDOFF_TIMEOUT_NS = 1
 FT_INJECT_MALLOC, FT_INJECT_REGISTER = 1, 2
 FT_HOST_PINNED, FT_HOST_HUGE_PAGES = 0, 1
+FT_KV_BF16, FT_KV_MXFP8, FT_KV_MXFP4 = 0, 1, 2
+FT_DEVERR_BAD_INDEX = 0x10
 
 PROFILE_KINDS = ("control", "fill", "gate_up", "down_combine", "prefill_route", "prefill_gemm_gate_up",
                  "prefill_combine", "prefill_copy", "prefill_gemm_down", "router")
@@ -78,6 +80,21 @@ class ft_profile(C.Structure):
     _fields_ = [("launches", C.c_uint64 * 10), ("total_ms", C.c_double * 10)]
 
 
+class ft_kv_cache(C.Structure):
+    _fields_ = [("kv_type", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("page_size", C.c_int),
+                ("n_pages", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p)]
+
+
+class ft_attn_args(C.Structure):
+    _fields_ = [("n_heads", C.c_int), ("n_tokens", C.c_int), ("n_seqs", C.c_int), ("max_new", C.c_int),
+                ("table_stride", C.c_int), ("causal", C.c_int), ("window", C.c_int), ("scale", C.c_float),
+                ("q", C.c_void_p), ("q_stride", C.c_longlong), ("q_start", C.c_void_p), ("kv_len", C.c_void_p),
+                ("page_table", C.c_void_p), ("out", C.c_void_p), ("out_stride", C.c_longlong),
+                ("lse", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("error_word_out", C.c_void_p)]
+
+
 _P = C.c_void_p
 _SIGS = {
     "ft_moe_init": [C.POINTER(ft_moe_config), C.POINTER(ft_banks), C.POINTER(ft_banks), C.POINTER(C.c_void_p)],
@@ -112,6 +129,10 @@ _SIGS = {
     "ft_host_free": [_P],
     "ft_moe_decode_resident_noalloc": [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, _P, _P, C.c_int, _P, _P, _P, _P,
                                        _P, _P],
+    "ft_kv_write": [C.POINTER(ft_kv_cache), C.c_int, _P, _P, C.c_longlong, C.c_longlong, _P, _P, _P],
+    "ft_kv_read": [C.POINTER(ft_kv_cache), C.c_int, _P, _P, _P, C.c_longlong, C.c_longlong, _P, _P],
+    "ft_attn_workspace": [C.c_int, C.c_int, C.c_int, C.POINTER(C.c_size_t)],
+    "ft_attn": [C.POINTER(ft_kv_cache), C.POINTER(ft_attn_args), _P],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -371,3 +392,96 @@ def make_config(n_layers, hidden, inter, n_experts, top_k, has_shared, wtype, ma
     return ft_moe_config(n_layers, hidden, inter, n_experts, top_k, int(has_shared), wtype, max_batch,
                          max_prefill_tokens, cache_slots, bp_gbps, bh_gbps, fill_mode, device,
                          compute_stream, transfer_stream)
+
+
+# ----------------------------------------------- paged key/value cache (include/ft_kv.h)
+def _dense(what, t, shape, itemsize) -> None:
+    """Raises unless tensor t has this shape (None: any size), element size and C order."""
+    if t.element_size() != itemsize or t.dim() != len(shape) or not t.is_contiguous() or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {list(shape)} with {itemsize}-byte elements, "
+                         f"got {list(t.shape)} of {t.dtype}")
+
+
+def _rows(what, t, heads, dim) -> int:
+    """Token stride of [n][heads][dim] 16-bit rows that are each contiguous."""
+    if t.element_size() != 2 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (
+            t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+        raise ValueError(f"{what}: expected rows of [{heads}][{dim}] BF16 elements, got {list(t.shape)} of {t.dtype} "
+                         f"with strides {list(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_scale=None, v_scale=None) -> ft_kv_cache:
+    """One layer's cache over torch tensors that the caller keeps: k, v [n_pages][n_kv_heads][page_size][elements of
+    a row] (BF16 elements, or bytes), scales [n_pages][n_kv_heads][page_size][head_dim // 32] bytes."""
+    per = {FT_KV_BF16: head_dim, FT_KV_MXFP8: head_dim, FT_KV_MXFP4: head_dim // 2}.get(kv_type)
+    if per is None:
+        raise ValueError(f"kv_type = {kv_type}")
+    lead = (n_pages, n_kv_heads, page_size)
+    for name, t in (("k", k), ("v", v)):
+        _dense(name, t, (*lead, per), 2 if kv_type == FT_KV_BF16 else 1)
+    if kv_type == FT_KV_BF16:
+        k_scale = v_scale = None
+    else:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None:
+                raise ValueError(f"{name} is missing")
+            _dense(name, t, (*lead, head_dim // 32), 1)
+    c = ft_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def ft_kv_write(cache, k, v, slots, error_word=None, stream=None) -> None:
+    """k, v: torch BF16 [n][n_kv_heads][head_dim], rows contiguous (parts of a wider tensor are fine); slots: int32 [n]."""
+    ks, vs = (_rows(w, t, cache.n_kv_heads, cache.head_dim) for w, t in (("k", k), ("v", v)))
+    _dense("slots", slots, (k.shape[0],), 4)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
+    _check(_lib.ft_kv_write(C.byref(cache), k.shape[0], k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(),
+                            _ptr(error_word), stream))
+
+
+def ft_kv_read(cache, slots, k_out, v_out, error_word=None, stream=None) -> None:
+    """The rows of `slots` as BF16 into k_out, v_out (laid out as ft_kv_write's k and v)."""
+    ks, vs = (_rows(w, t, cache.n_kv_heads, cache.head_dim) for w, t in (("k_out", k_out), ("v_out", v_out)))
+    _dense("slots", slots, (k_out.shape[0],), 4)
+    if v_out.shape[0] != k_out.shape[0]:
+        raise ValueError(f"k_out has {k_out.shape[0]} tokens, v_out {v_out.shape[0]}")
+    _check(_lib.ft_kv_read(C.byref(cache), k_out.shape[0], slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ks, vs,
+                           _ptr(error_word), stream))
+
+
+def ft_attn_workspace(n_heads, n_kv_heads, head_dim) -> int:
+    n = C.c_size_t()
+    _check(_lib.ft_attn_workspace(n_heads, n_kv_heads, head_dim, C.byref(n)))
+    return n.value
+
+
+def make_attn_args(n_heads, max_new, q, q_start, kv_len, page_table, out, workspace, scale, window=0, causal=True,
+                   lse=None, error_word=None) -> ft_attn_args:
+    """Arguments of ft_attn over torch tensors that the caller keeps; they can be used again while the tensors' contents
+    change.  q, out: BF16 [n_tokens][n_heads][head_dim], rows contiguous; q_start int32 [n_seqs + 1]; kv_len int32
+    [n_seqs]; page_table int32 [n_seqs][pages]; lse FP32 [n_tokens][n_heads] or None."""
+    n, dim = q.shape[0], q.shape[-1]
+    qs, os_ = _rows("q", q, n_heads, dim), _rows("out", out, n_heads, dim)
+    if out.shape[0] != n:
+        raise ValueError(f"q has {n} tokens, out {out.shape[0]}")
+    seqs = kv_len.shape[0]
+    _dense("kv_len", kv_len, (None,), 4)
+    _dense("q_start", q_start, (seqs + 1,), 4)
+    _dense("page_table", page_table, (seqs, None), 4)
+    if lse is not None:
+        _dense("lse", lse, (n, n_heads), 4)
+    a = ft_attn_args(n_heads, n, seqs, max_new, page_table.shape[1], int(bool(causal)), window, scale, _ptr(q), qs,
+                     _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(out), os_, _ptr(lse), _ptr(workspace),
+                     workspace.numel() * workspace.element_size(), _ptr(error_word))
+    a.tensors, a.head_dim = (q, q_start, kv_len, page_table, out, workspace, lse, error_word), dim
+    return a
+
+
+def ft_attn(cache, args, stream=None) -> None:
+    if args.head_dim != cache.head_dim:
+        raise ValueError(f"q has rows of {args.head_dim}, the cache of {cache.head_dim}")
+    _check(_lib.ft_attn(C.byref(cache), C.byref(args), stream))
