@@ -7,8 +7,11 @@ namespace ft {
 namespace kv {
 
 cudaError_t attn_rows_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s);
 cudaError_t attn_rows_mxfp8(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_mxfp8(const AttnParams& p, int D, int n_sm, cudaStream_t s);
 cudaError_t attn_rows_mxfp4(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_mxfp4(const AttnParams& p, int D, int n_sm, cudaStream_t s);
 
 namespace {
 
@@ -27,8 +30,9 @@ int sm_count() {
   return n;
 }
 
-// Counters, and two partial results for each CTA: 16 rows of head_dim + 2 floats, two CTAs per SM.
-size_t workspace_need(int n_sm, int D) { return kCounterBytes + (size_t)n_sm * 2 * 2 * 16 * (D + 2) * 4; }
+// Counters, a stand-in for the caller's error word, and two partial results for each CTA: of
+// head_dim + 2 floats for 16 rows (few rows: two CTAs per SM), or 256 or 128 rows (chunks: one).
+size_t workspace_need(int n_sm, int D) { return kCounterBytes + 256 + (size_t)n_sm * 2 * (D == 256 ? 128 : 256) * (D + 2) * 4; }
 
 ft_status check_heads(const char* name, int n_heads, int n_kv_heads, int head_dim) {
   if (n_kv_heads < 1 || n_kv_heads > 1024 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128)
@@ -111,11 +115,13 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   p.out_stride = a->out_stride;
   p.lse = a->lse;
   p.counters = static_cast<uint32_t*>(a->workspace);
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kv::kCounterBytes);
-  p.error_word = a->error_word_out;
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kv::kCounterBytes + 256);
+  p.error_word = a->error_word_out ? a->error_word_out : p.counters + kv::kMaxCtas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = c->kv_type == FT_KV_BF16    ? kv::attn_rows_bf16(p, c->head_dim, n_sm, s)
-                        : c->kv_type == FT_KV_MXFP8 ? kv::attn_rows_mxfp8(p, c->head_dim, n_sm, s)
-                                                    : kv::attn_rows_mxfp4(p, c->head_dim, n_sm, s);
+  using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, cudaStream_t);
+  static const Kernel kernels[2][3] = {{kv::attn_rows_bf16, kv::attn_rows_mxfp8, kv::attn_rows_mxfp4},
+                                       {kv::attn_chunk_bf16, kv::attn_chunk_mxfp8, kv::attn_chunk_mxfp4}};
+  const bool many = (long long)a->max_new * p.group > 32;  // rows of one cache head
+  const cudaError_t e = kernels[many][c->kv_type](p, c->head_dim, n_sm, s);
   return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }

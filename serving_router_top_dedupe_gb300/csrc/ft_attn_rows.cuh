@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       if (wanted(k + 1)) page_next = __ldg(table + ((t + UT) >> p.page_shift));
       if (wanted(k)) {
         const bool ok = (unsigned)page < (unsigned)p.n_pages;
-        if (!ok && lane == 0 && p.error_word) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+        if (!ok && lane == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
         const int r0 = max(cur.lo - t, 0), r1 = ok ? min(cur.hi - t, CHUNK) : 0;  // rows to read; the others are zeros
         const long long row = (((long long)(ok ? page : 0) * p.n_kv_heads + cur.head) << p.page_shift) +
                               (t & (p.page_size - 1));
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
           cp_async16(dst + piece<C::rby>(r, pc), ksrc + u * 16, there);
           cp_async16(dst + C::kv_bytes + piece<C::rby>(r, pc), vsrc + u * 16, there);
         }
-        if (TYPE != FT_KV_BF16) {  // scales of all 16 rows
+        if constexpr (TYPE != FT_KV_BF16) {  // scales of all 16 rows
           constexpr int PS = CHUNK * C::sby / 16;
           if (lane < 2 * PS) {
             const int i = lane % PS;

@@ -53,7 +53,7 @@ struct AttnParams {
   float* lse;
   uint32_t* counters;  // [kMaxCtas], zero between calls
   float* partials;
-  uint32_t* error_word;
+  uint32_t* error_word;  // never NULL
 };
 
 constexpr int kMaxCtas = 4096;                     // CTAs of one attention launch, at most
@@ -164,7 +164,7 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, Cursor& cur, long long& 
     }
     sm.sum[s] = sum;
   }
-  if (any_bad && blockIdx.x == 0 && p.error_word) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+  if (any_bad && blockIdx.x == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
   if (tid == 0) sm.found = -1;
   many = __syncthreads_or(many);
   // sequences of many blocks: a warp counts each

@@ -292,3 +292,21 @@ def test_bad_lengths_and_pages_are_reported(F):
     b.dev[1][0] = -3
     out, lse = b.run()
     assert b.word.item() == F.FT_DEVERR_BAD_INDEX and np.all(out[0] == 0) and np.all(lse[0] == -np.inf)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim,page", [(16, 2, 256, 128), (32, 4, 128, 64), (24, 8, 64, 16)])
+@pytest.mark.parametrize("length", [1000, 6001])
+def test_kernels_for_few_and_for_many_rows_agree(F, kind, heads, kv_heads, dim, page, length):
+    """Many items, several to a CTA and several CTAs to an item: both kernels within twice the tolerance of each other
+    (each is within one of the definition), and the same bits again."""
+    a, b, c = (Batch(F, kind, heads, kv_heads, dim, page, new=[500, 33], lens=[length, 400], max_new=m) for m in (1, 500, 500))
+    (o1, l1), (o2, l2), (o3, l3) = a.run(), b.run(), c.run()
+    o4, l4 = c.run()
+    assert np.array_equal(o2, o3) and np.array_equal(l2, l3) and np.array_equal(o2, o4) and np.array_equal(l2, l4)
+    assert a.word.item() == b.word.item() == 0
+    k, v = (np.nanmax(np.abs(x)) for x in a.cache.value)
+    d = 1.01 * (dim + 4) * 2.0 ** -24 * a.scale * k * np.abs(a.q).sum(-1).max()
+    tol = 2.0 ** -8 * np.abs(o1) + (2.0 ** -8 + 2 * d + 2.0 ** -20) * v
+    assert np.all(np.abs(o1 - o2) <= 2 * tol)
+    assert np.all(np.abs(l1 - l2) <= 2 * (d + 2.0 ** -20 * (1 + np.abs(l1))))
