@@ -87,7 +87,8 @@ ft_status ft_kv_read(const ft_kv_cache* cache, int n_tokens, const int32_t* slot
  * tokens) does not matter, NaN and infinities included. */
 typedef struct {
   int n_heads;              /* query heads, a multiple of n_kv_heads; at most 128 per cache head */
-  int n_tokens;             /* new tokens of the batch: rows of q, out and lse */
+  int n_tokens;             /* new tokens of the batch: rows of q, out and lse; n_tokens * n_heads below 2^31,
+                               and n_tokens * (n_heads / n_kv_heads) below 2^25 */
   int n_seqs;               /* sequences, at most 1024 */
   int max_new;              /* new tokens of one sequence, at most: chooses the kernel, and any value >= 1
                                gives the same results within rounding */

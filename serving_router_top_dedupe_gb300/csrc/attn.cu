@@ -63,7 +63,8 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   if (!a) return kv_fail(FT_ERR_INVALID, "%s: args is NULL", name);
   if (ft_status st = kv::check_heads(name, a->n_heads, c->n_kv_heads, c->head_dim)) return st;
   if (a->n_tokens < 0 || a->n_seqs < 0 || a->n_seqs > kv::kMaxSeqs || a->max_new < 1 ||
-      (long long)a->n_tokens * a->n_heads >= (1ll << 31))
+      (long long)a->n_tokens * a->n_heads >= (1ll << 31) ||
+      (long long)a->n_tokens * (a->n_heads / c->n_kv_heads) >= kv::kMaxRows)
     return kv_fail(FT_ERR_INVALID, "%s: n_tokens = %d, n_seqs = %d, max_new = %d", name, a->n_tokens, a->n_seqs,
                    a->max_new);
   if (a->table_stride < 1 || (long long)a->table_stride * c->page_size > (1ll << 30) || a->window < 0 ||
@@ -100,6 +101,7 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   p.n_kv_heads = c->n_kv_heads;
   p.n_heads = a->n_heads;
   p.group = a->n_heads / c->n_kv_heads;
+  p.group_magic = p.group == 1 ? 0 : (uint32_t)((1ull << 32) / p.group + ((1ull << 32) % p.group != 0));
   p.n_tokens = a->n_tokens;
   p.n_seqs = a->n_seqs;
   p.table_stride = a->table_stride;

@@ -13,7 +13,7 @@
 // row's thread then does that itself.
 //
 // Warps 0-3 (and 4-7): softmax, output.  Then one warp that issues every MMA, and the loaders:
-// two warps of TMA (K, V) for a BF16 cache, four warps that decode into the same layout for a
+// two warps of TMA (K, V) for a BF16 cache, eight warps that decode into the same layout for a
 // quantised one.
 #pragma once
 
@@ -36,6 +36,8 @@ using rows::pack;
 
 constexpr int KT = 128;           // cached tokens of a tile
 constexpr int PANEL = KT * 128;   // bytes of 64 columns of a tile: rows of 128 bytes, 128-byte swizzle
+constexpr int kLeast = 4;         // counts of a CTA's share, at least
+constexpr int OV = 2;             // counts of an item besides its tiles
 constexpr float kSlack = 8.f;     // log2 units by which scores may pass the running maximum
 
 template <int TYPE, int D>
@@ -47,10 +49,20 @@ struct Cfg {
   static constexpr int stage = panels * PANEL;
   static constexpr int stages = D == 64 ? 4 : D == 128 ? 2 : 1;  // of K, and of V
   static constexpr int soft_warps = 4 * tiles;
-  static constexpr int mma_warp = soft_warps, load_warp = q ? soft_warps + 4 : soft_warps + 1;
-  static constexpr int threads = 32 * (soft_warps + (q ? 8 : 4));
+  static constexpr int mma_warp = soft_warps, load_warp = soft_warps + 4;
+  static constexpr int threads = 32 * (soft_warps + (q ? 12 : 4));
   static constexpr int qbytes = tiles * stage;
-  static constexpr int smem = 1024 + qbytes + 2 * stages * stage + 512;
+  static constexpr int out_bytes = soft_warps * 32 * 128;  // 64 output columns of each warp's rows
+  static constexpr int smem = 1024 + qbytes + 2 * stages * stage + out_bytes + 512;
+  // Registers of the softmax, MMA and loader warps out of those that the block starts with:
+  // BF16, two tiles (168 x 384 = 64512): 208 x 256 + 88 x 128 = 64512;
+  // quantised, two tiles (96 x 640 = 61440): 136 x 256 + 80 x 128 + 64 x 256 = 61440;
+  // quantised, one tile (128 x 512 = 65536): 192 x 128 + 96 x 128 + 112 x 256 = 65536.
+  static constexpr bool split = q || tiles == 2;
+  static constexpr int soft_regs = !q ? 208 : tiles == 2 ? 136 : 192;
+  static constexpr int mma_regs = !q ? 88 : tiles == 2 ? 80 : 96;
+  static constexpr int load_regs = tiles == 2 ? 64 : 112;
+  static constexpr int batch = !q && tiles == 2 ? 128 : 64;  // score columns that a softmax thread holds
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
   static constexpr int o_col = 256;  // TMEM: S (and P) at 0 and 128, O behind
 };
@@ -59,16 +71,30 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: 8-row atoms of 1024 bytes (stride byte
 // offset); lead: bytes from one 64-column panel to the next, for the operand whose columns
-// run along the 128-byte rows (V), unused by the other (Q, K).
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// run along the 128-byte rows (V), unused by the other (Q, K).  desc_lo is the low word, to
+// which offsets / 16 may be added.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+  uint32_t lo = ((saddr & 0x3FFFFu) >> 4) | (lead >> 4) << 16;
+  asm volatile("" : "+r"(lo));  // formed where it is used: the issuing thread has few registers
+  return lo;
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+  return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
 }
 
 // Instruction descriptor, kind::f16: BF16 operands, FP32 accumulator; bt: B's columns contiguous.
@@ -91,33 +117,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// 32 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tld32(uint32_t a, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(a));
+// N consecutive 32-bit columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void tld(uint32_t a, uint32_t* r) {
+  static_assert(N == 32, "columns of a load");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(a));
 }
-__device__ __forceinline__ void tst16(uint32_t a, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tst32(uint32_t a, const uint32_t* r) {
-  tst16(a, r);
-  tst16(a + 16, r + 16);
+template <int N>
+__device__ __forceinline__ void tst(uint32_t a, const uint32_t* r) {
+  static_assert(N == 32, "columns of a store");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 // The loaded registers go through the wait, so that nothing reads them earlier.
+template <int N>
 __device__ __forceinline__ void tld_wait(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -147,23 +166,8 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int 
       : "memory");
 }
 
-// A position in the CTA's sequence of tiles.
 template <int TYPE, int D>
-struct Walk {
-  Cursor cur;
-  long long w, w1;
-  __device__ __forceinline__ int tile() const { return cur.t0 + (int)(w - cur.start); }
-  __device__ __forceinline__ bool first() const { return w == cur.start; }
-  // Next tile; true when it is one of another item.
-  __device__ __forceinline__ bool next(const AttnParams& p) {
-    ++w;
-    if (w < w1 && w == cur.start + cur.cost) {
-      cursor_next<Cfg<TYPE, D>::RB, KT>(p, cur);
-      return true;
-    }
-    return false;
-  }
-};
+using ChunkWalk = Walk<Cfg<TYPE, D>::RB, KT, OV>;
 
 // 16 bytes of codes -> 16 (MXFP8) or 32 (MXFP4) BF16 values in their order.
 template <int TYPE>
@@ -193,45 +197,75 @@ __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
     out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
-// 16-byte pieces of a tile's codes that one loader thread holds, and their scale codes.
+// Page ids of a tile: lane i (and i + 8, ...) holds that of tokens [t + 16 i, t + 16 i + 16), or
+// -1 where no row sees them.
+__device__ __forceinline__ int tile_pages(const AttnParams& p, const Cursor& cur, int t, int lane) {
+  const int tok = t + 16 * (lane & 7);
+  if (tok >= cur.len || tok + 16 <= cur.lo) return -1;
+  const int page = __ldg(p.page_table + (long long)cur.seq * p.table_stride + (tok >> p.page_shift));
+  if ((unsigned)page < (unsigned)p.n_pages) return page;
+  atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+  return -1;
+}
+
+// 16-byte pieces of a tile's codes that one loader thread holds: piece lt % PR of rows
+// (lt + 128 i) / PR.  A warp's pieces belong to 32 rows, and lane l holds the scale codes of
+// the l-th of them (zero where nothing is seen: the codes loaded for such a row, from some
+// other place of the cache, then stand for zeros).
 template <int TYPE, int D>
 struct Raw {
   static constexpr int PR = row_bytes(TYPE, D) / 16;  // pieces of a row, and of a thread
   uint4 w[PR];
-  uint32_t sc[PR];
+  uint32_t sc[D == 256 ? 2 : 1];
 };
 
 template <int TYPE, int D>
-__device__ __forceinline__ void raw_load(const AttnParams& p, const Cursor& cur, int t, const uint8_t* base,
+__device__ __forceinline__ void raw_load(const AttnParams& p, const Cursor& cur, int t, int pages, const uint8_t* base,
                                          const uint8_t* scales, int lt, Raw<TYPE, D>& x) {
   constexpr int PR = Raw<TYPE, D>::PR;
-  const int32_t* table = p.page_table + (long long)cur.seq * p.table_stride;
+  const int lane = lt & 31, in_page = p.page_size - 1;
+  auto row_at = [&](int r, int page) {  // row of the cache; a page that is not there: some row
+    return ((max(page, 0) * p.n_kv_heads + cur.head) << p.page_shift) + ((t + r) & in_page);
+  };
 #pragma unroll
   for (int i = 0; i < PR; ++i) {
-    const int u = lt + 128 * i, tok = t + u / PR, pc = u % PR;
-    x.w[i] = make_uint4(0, 0, 0, 0);
-    x.sc[i] = 0;
-    if (tok < cur.len && tok >= cur.lo) {
-      const int page = __ldg(table + (tok >> p.page_shift));
-      if ((unsigned)page < (unsigned)p.n_pages) {
-        const long long row = (((long long)page * p.n_kv_heads + cur.head) << p.page_shift) + (tok & (p.page_size - 1));
-        x.w[i] = __ldg(reinterpret_cast<const uint4*>(base + row * row_bytes(TYPE, D)) + pc);
-        x.sc[i] = __ldg(scales + row * (D / 32) + (TYPE == FT_KV_MXFP8 ? pc / 2 : pc));
-      } else {
-        atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
-      }
-    }
+    const int u = lt + 128 * i, r = u / PR;
+    const int row = row_at(r, __shfl_sync(0xffffffffu, pages, r >> 4));
+    x.w[i] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)(uint32_t)row * row_bytes(TYPE, D)) + u % PR);
+  }
+  constexpr int per = 32 / PR;  // rows of a warp's piece i
+  const int r = ((lt & ~31) + 128 * (lane / per)) / PR + lane % per;
+  const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
+  const bool seen = page >= 0 && t + r < cur.len && t + r >= cur.lo;
+  const uint8_t* src = scales + (size_t)(uint32_t)row_at(r, page) * (D / 32);
+  if constexpr (D == 64) {
+    const uint32_t s = __ldg(reinterpret_cast<const uint16_t*>(src));
+    x.sc[0] = seen ? s : 0u;
+  } else if constexpr (D == 128) {
+    const uint32_t s = __ldg(reinterpret_cast<const uint32_t*>(src));
+    x.sc[0] = seen ? s : 0u;
+  } else {
+    const uint2 s = __ldg(reinterpret_cast<const uint2*>(src));
+    x.sc[0] = seen ? s.x : 0u;
+    x.sc[1] = seen ? s.y : 0u;
   }
 }
 
 template <int TYPE, int D>
 __device__ __forceinline__ void raw_store(uint8_t* stage, int lt, const Raw<TYPE, D>& x) {
   constexpr int PR = Raw<TYPE, D>::PR, OUT = TYPE == FT_KV_MXFP8 ? 2 : 4;  // 16-byte pieces of BF16 for one of codes
+  constexpr int per = 32 / PR;
+  const int lane = lt & 31, pc = lt % PR, blk = TYPE == FT_KV_MXFP8 ? pc / 2 : pc;
 #pragma unroll
   for (int i = 0; i < PR; ++i) {
-    const int u = lt + 128 * i, r = u / PR, pc = u % PR;
+    const int r = (lt + 128 * i) / PR, from = i * per + lane / PR;
+    uint32_t s = __shfl_sync(0xffffffffu, x.sc[0], from);
+    if constexpr (D == 256) {
+      const uint32_t s1 = __shfl_sync(0xffffffffu, x.sc[1], from);
+      s = blk < 4 ? s : s1;
+    }
     uint4 o[OUT];
-    decode16<TYPE>(x.w[i], x.sc[i], o);
+    decode16<TYPE>(x.w[i], (s >> (8 * (blk & 3))) & 0xffu, o);
 #pragma unroll
     for (int j = 0; j < OUT; ++j) {
       const int ch = pc * OUT + j;
@@ -248,7 +282,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + C::qbytes;  // K stages, then V stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + 2 * NS * C::stage);
+  uint8_t* out_stage = ring + 2 * NS * C::stage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + C::out_bytes);
   uint64_t* full = bars;              // [2][NS] a tile of K, of V is in the ring
   uint64_t* empty = bars + 2 * NS;    // [2][NS] its products are done
   uint64_t* q_full = bars + 4 * NS;   // [2] the queries of a row tile are in place
@@ -278,9 +313,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     *abort_flag = 0;
     ptx::mbar_fence_init();
   }
-  Walk<TYPE, D> wk;
+  ChunkWalk<TYPE, D> wk;
   long long per;
-  if (!plan<C::RB, KT, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), wk.cur, wk.w, wk.w1, per)) return;
+  if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kLeast, wk, per)) return;
   if (warp == C::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(tmem_slot))
                  : "memory");
@@ -290,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot, q_addr = ptx::smem_u32(smem);
   auto wait = [&](uint64_t* b, uint32_t parity) { return ptx::mbar_wait(bar(b), parity, abort_flag, p.error_word); };
   // for a whole warp: all its lanes go on, or none
   auto wait_all = [&](uint64_t* b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(b, parity)); };
@@ -299,85 +334,153 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
 
   if (warp < C::soft_warps) {
     // ------------------------------------------------------------------ softmax and output
+    if (C::split) regs_up<C::soft_regs>();
     const int rt = warp >> 2;              // row tile
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_tm = tl + C::o_col + rt * D;
     const float c = fabsf(p.scale_log2) * left_in(TYPE);
     const uint64_t c2 = f2(c, c);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale turns the queries' signs
 
     // an item's queries into shared memory, once no product reads the last ones
     auto load_q = [&](const Cursor& cur) {
       const int rows = rows_of(cur, rt);
       if (rows <= 0) return;
-      const int rr = cur.rb * C::RB + 128 * rt + r, tok = rr / p.group, hd = rr - tok * p.group;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(cur.q0 + tok) * p.q_stride +
-                                                        (long long)(cur.head * p.group + hd) * D);
-      uint8_t* dst = smem + rt * C::stage + r * 128;
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) v = __ldg(src + i);
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * PANEL + (((i & 7) ^ (r & 7)) << 4)) =
-            r < rows ? make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip) : v;
+      constexpr int PQ = D / 8;  // 16-byte pieces of a row
+      const int row0 = cur.rb * C::RB + 128 * rt, wt = tid & 127;
+      const uint16_t* src = p.q + (long long)cur.q0 * p.q_stride + (long long)cur.head * p.group * D;
+      const uint32_t dst = q_addr + rt * C::stage;
+      auto at = [&](int u) {
+        const int x = u / PQ, pc = u % PQ;
+        return (uint32_t)((pc >> 3) * PANEL + x * 128 + (((pc & 7) ^ (x & 7)) << 4));
+      };
+#pragma unroll 4
+      for (int i = 0; i < PQ; ++i) {
+        const int u = wt + 128 * i, x = u / PQ, pc = u % PQ;
+        const int tok = div_group(p, row0 + x), hd = row0 + x - tok * p.group;
+        rows::cp_async16(dst + at(u), x < rows ? src + tok * p.q_stride + hd * D + pc * 8 : p.q, x < rows);
       }
+      rows::cp_commit();
+      rows::cp_wait<0>();
+      if (p.scale_log2 < 0.f)  // a negative scale turns the queries' signs
+        for (int i = 0; i < PQ; ++i) {
+          uint4* v = reinterpret_cast<uint4*>(smem + rt * C::stage + at(wt + 128 * i));
+          *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
+        }
       fence_async();
       ptx::mbar_arrive(bar(q_full + rt));
+    };
+    // 64 normalised output columns of the warp's rows, from the lanes' rows to rows in memory:
+    // w: this row's 32 words of BF16 pairs
+    uint8_t* stg = out_stage + warp * 4096;
+    auto put_out = [&](const Cursor& cur, int rows, int col, const uint32_t* w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = 4 * i + (lane >> 3), row = (warp & 3) * 32 + x, pc = lane & 7;
+        if (row < rows) {
+          const int rr = cur.rb * C::RB + 128 * rt + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
+          *reinterpret_cast<uint4*>(p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D + col + pc * 8) =
+              *reinterpret_cast<const uint4*>(stg + x * 128 + ((pc ^ (x & 7)) << 4));
+        }
+      }
+      __syncwarp();
     };
 
     uint32_t s_ph = 0, pvs = 0;  // phases of s_full (bit u); products with V so far
     uint32_t step = 0;
     bool ok = true;
     load_q(wk.cur);
-    while (ok && wk.w < wk.w1) {  // one item
+    while (ok && wk.more()) {  // one item
       const Cursor cur = wk.cur;
       const int rows = rows_of(cur, rt);
       const int rbase = cur.rb * C::RB + 128 * rt;
-      int lo = 0, hi = 0, lo_max = 0, hi_min = 0;
+      // what this row sees: [lo, hi); what every row of the tile sees: [lo_max, hi_min)
+      int lo = 0, hi = 1 << 30, lo_max = 0, hi_min = 0;
       if (rows > 0) {
         auto see = [&](int row, int& a, int& b) {
-          const int pos = cur.len - cur.n + row / p.group;
-          b = p.causal ? min(cur.len, pos + 1) : cur.len;
+          const int pos = cur.len - cur.n + div_group(p, row);
           a = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+          b = max(p.causal ? min(cur.len, pos + 1) : cur.len, a);
         };
+        if (r < rows) see(rbase + r, lo, hi);  // rows that are not there see everything
         int x;
-        see(rbase + r, lo, hi);
         see(rbase, x, hi_min);
         see(rbase + rows - 1, lo_max, x);
       }
       float m = -INFINITY, l = 0.f;
       bool first = true;  // no product with V yet
-      const long long end = min(cur.start + cur.cost, wk.w1);
-      for (; wk.w < end; ++wk.w, ++step) {
-        if (rows <= 0) continue;
+      const int steps = (int)(wk.end() - wk.w);
+      int t = wk.tile() * KT;
+      for (int j = 0; j < steps && rows > 0; ++j, ++step, t += KT) {
         const int u = T == 2 ? rt : (int)(step & 1);
         const uint32_t s_tm = tl + 128 * u;
         if (!(ok = wait_all(s_full + u, (s_ph >> u) & 1))) break;
         s_ph ^= 1u << u;
         tc_after();
-        const int t = wk.tile() * KT;
         const bool edge = t < lo_max || t + KT > hi_min;
-        const int e_lo = lo - t, e_hi = hi - t;  // columns [e_lo, e_hi) are seen
-        auto mask = [&](uint32_t* s, int ch) {
+        // scores that this row does not see become -inf
+        auto mask = [&](uint32_t* s, int col, int n) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * ch + i < e_lo || 32 * ch + i >= e_hi) s[i] = 0xff800000u;
+          for (int c16 = 0; c16 < n; c16 += 16) {
+            const int a = t + col + c16;
+            if (a >= lo_max && a + 16 <= hi_min) continue;  // every row of the tile sees these
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((uint32_t)(a + i - lo) >= (uint32_t)(hi - lo)) s[c16 + i] = 0xff800000u;
+          }
         };
+        constexpr int BC = C::batch;  // columns read from TMEM at once
+        uint32_t pr[64];
         float mx = -INFINITY;
-        uint32_t s[2][32];
-        tld32(s_tm, s[0]);
+        uint64_t sum0, sum1;
+        if (first) {  // the first maximum
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tld_wait(s[ch & 1]);
-          if (ch < 3) tld32(s_tm + 32 * (ch + 1), s[(ch + 1) & 1]);
-          if (edge) mask(s[ch & 1], ch);
+          for (int b = 0; b < KT / BC; ++b) {
+            uint32_t s[BC];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[ch & 1][i]));
+            for (int i = 0; i < BC; i += 32) tld<32>(s_tm + b * BC + i, s + i);
+            tld_wait<BC>(s);
+            if (edge) mask(s, b * BC, BC);
+#pragma unroll
+            for (int i = 0; i < BC; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+          }
+          m = mx * c;
+          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or only NaN
         }
-        tld32(s_tm, s[0]);
-        mx *= c;
-        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+        for (;;) {
+          // probabilities against the running maximum as it is; a score that passes it by too
+          // much is found on the way and starts the tile again
+          const float mu = m == -INFINITY ? 0.f : m;
+          const uint64_t nm = f2(-mu, -mu);
+          sum0 = sum1 = 0;
+          mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < KT / BC; ++b) {
+            uint32_t s[BC];
+#pragma unroll
+            for (int i = 0; i < BC; i += 32) tld<32>(s_tm + b * BC + i, s + i);
+            tld_wait<BC>(s);
+            if (edge) mask(s, b * BC, BC);
+#pragma unroll
+            for (int i = 0; i < BC / 2; ++i) {
+              const float x = __uint_as_float(s[2 * i]), y = __uint_as_float(s[2 * i + 1]);
+              mx = fmaxf(mx, fmaxf(x, y));
+              float e0, e1;
+              unf2(fma2(f2(x, y), c2, nm), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              if (i & 1) sum1 = add2(sum1, f2(e0, e1));
+              else sum0 = add2(sum0, f2(e0, e1));
+              pr[b * BC / 2 + i] = pack(e0, e1);
+            }
+          }
+          mx *= c;
+          if (!__any_sync(0xffffffffu, mx > m + kSlack)) break;
           const float mn = fmaxf(m, mx);
           const float al = mn == -INFINITY ? 1.f : ex2(m - mn);
           l *= al;
@@ -385,39 +488,20 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
           if (!first) {
             if (!(ok = wait_all(o_full + rt, (pvs - 1) & 1))) break;
             tc_after();
-            tld_wait(s[0]);
             uint32_t o[32];
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
-              tld32(o_tm + 32 * ch, o);
-              tld_wait(o);
+              tld<32>(o_tm + 32 * ch, o);
+              tld_wait<32>(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tst32(o_tm + 32 * ch, o);
+              tst<32>(o_tm + 32 * ch, o);
             }
           }
         }
-        const float mu = m == -INFINITY ? 0.f : m;
-        const uint64_t nm = f2(-mu, -mu);
-        uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tld_wait(s[ch & 1]);
-          if (ch < 3) tld32(s_tm + 32 * (ch + 1), s[(ch + 1) & 1]);
-          if (edge) mask(s[ch & 1], ch);
-          uint32_t pr[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float a, b;
-            unf2(fma2(f2(__uint_as_float(s[ch & 1][2 * i]), __uint_as_float(s[ch & 1][2 * i + 1])), c2, nm), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            if (i & 1) sum1 = add2(sum1, f2(a, b));
-            else sum0 = add2(sum0, f2(a, b));
-            pr[i] = pack(a, b);
-          }
-          tst16(s_tm + 16 * ch, pr);
-        }
+        if (!ok) break;
+        tst<32>(s_tm, pr);
+        tst<32>(s_tm + 32, pr + 32);
         tst_wait();
         // With two S buffers these scores do not tell that the product before last is done.  No
         // phase of o_full may be skipped: a parity tells a phase from its neighbours only.
@@ -432,37 +516,35 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       }
       if (!ok) break;
       // on to the next item: its queries first, so that its scores are formed during the output
-      if (wk.w < wk.w1) {
-        if (wk.w == cur.start + cur.cost) cursor_next<C::RB, KT>(p, wk.cur);
-        load_q(wk.cur);
-      }
+      wk.next_item(p);
+      if (wk.more()) load_q(wk.cur);
       if (rows <= 0) continue;
       if (!(ok = wait_all(o_full + rt, (pvs - 1) & 1))) break;
       tc_after();
       int ca, cb;
       piece_owners(cur, per, ca, cb);
-      const int tok = (rbase + r) / p.group, hd = cur.head * p.group + rbase + r - tok * p.group;
-      uint16_t* dst = p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D;
-      float* lse = p.lse + (long long)(cur.q0 + tok) * p.n_heads + hd;
+      float* lse = nullptr;
+      if (p.lse && r < rows) {
+        const int tok = div_group(p, rbase + r), hd = cur.head * p.group + rbase + r - tok * p.group;
+        lse = p.lse + (long long)(cur.q0 + tok) * p.n_heads + hd;
+      }
       if (ca == cb) {
         const float inv = l == 0.f ? 0.f : left_in(TYPE) / l;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          tld32(o_tm + 32 * ch, o);
-          tld_wait(o);
-          if (r < rows) {
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            tld<32>(o_tm + 64 * ch + 32 * h, o);
+            tld_wait<32>(o);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
-              reinterpret_cast<uint4*>(dst + 32 * ch)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int i = 0; i < 16; ++i)
+              w[16 * h + i] = pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
           }
+          put_out(cur, rows, 64 * ch, w);
         }
-        if (p.lse && r < rows) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+        if (lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       } else {
         // partial result: columns in groups of four, the rows of a group side by side
         const int me = blockIdx.x, at = 128 * rt + r;
@@ -470,8 +552,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t o[32];
-          tld32(o_tm + 32 * ch, o);
-          tld_wait(o);
+          tld<32>(o_tm + 32 * ch, o);
+          tld_wait<32>(o);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(reinterpret_cast<uint4*>(slot) + (8 * ch + i) * C::RB + at,
@@ -496,38 +578,39 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
                   (mm == -INFINITY ? 0.f : ex2(__ldcg(part(x) + C::RB * D + at) - mm));
           const float inv = ll == 0.f ? 0.f : left_in(TYPE) / ll;
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            float acc[32];
+          for (int ch = 0; ch < D / 64; ++ch) {
+            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int h = 0; h < 2; ++h) {
+              float acc[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[i] = 0.f;
 #pragma unroll 1
-            for (int x = ca; x <= cb; ++x) {
-              const float wx = mm == -INFINITY ? 0.f : ex2(__ldcg(part(x) + C::RB * D + at) - mm);
+              for (int x = ca; x <= cb; ++x) {
+                const float wx = mm == -INFINITY ? 0.f : ex2(__ldcg(part(x) + C::RB * D + at) - mm);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part(x)) + (8 * ch + i) * C::RB + at);
-                acc[4 * i] += v.x * wx;
-                acc[4 * i + 1] += v.y * wx;
-                acc[4 * i + 2] += v.z * wx;
-                acc[4 * i + 3] += v.w * wx;
+                for (int i = 0; i < 8; ++i) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(x)) + (16 * ch + 8 * h + i) * C::RB + at);
+                  acc[4 * i] += v.x * wx;
+                  acc[4 * i + 1] += v.y * wx;
+                  acc[4 * i + 2] += v.z * wx;
+                  acc[4 * i + 3] += v.w * wx;
+                }
               }
-            }
-            if (r < rows) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4*>(dst + 32 * ch)[i] =
-                    make_uint4(pack(acc[8 * i] * inv, acc[8 * i + 1] * inv), pack(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
-                               pack(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), pack(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+              for (int i = 0; i < 16; ++i) w[16 * h + i] = pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
             }
+            put_out(cur, rows, 64 * ch, w);
           }
-          if (p.lse && r < rows) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
+          if (lse) *lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
         }
       }
     }
-  } else if (warp == C::mma_warp) {
+  } else if (warp < C::soft_warps + 4) {
+    if (C::split) regs_down<C::mma_regs>();
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t q_addr = ptx::smem_u32(smem), ring_addr = ptx::smem_u32(ring);
+    if (warp == C::mma_warp && lane == 0) {
+      const uint32_t ring_addr = ptx::smem_u32(ring);
       uint32_t kst = 0, vst = 0, kph = 0, vph = 0;  // ring positions and phases
       uint32_t q_ph = 0, p_ph = 0;
       auto advance = [&](uint32_t& st, uint32_t& ph) {
@@ -538,19 +621,19 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       };
       // scores of row tile x into S buffer u, from the K stage at kst
       auto scores = [&](int x, int u) {
-        const uint32_t a = q_addr + x * C::stage, b = ring_addr + kst * C::stage;
+        const uint32_t a = desc_lo(q_addr + x * C::stage, 0), b = desc_lo(ring_addr + kst * C::stage, 0);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * PANEL + 32 * (k & 3);
-          mma_ss(tmem + 128 * u, desc(a + off, 0), desc(b + off, 0), idesc(128, KT, 0), k != 0);
+          const uint32_t off = ((k >> 2) * PANEL + 32 * (k & 3)) >> 4;
+          mma_ss(tmem + 128 * u, desc(a + off), desc(b + off), idesc(128, KT, 0), k != 0);
         }
         commit(bar(s_full + u));
       };
       auto product = [&](int x, int u, bool first) {
-        const uint32_t b = ring_addr + (NS + vst) * C::stage;
+        const uint32_t b = desc_lo(ring_addr + (NS + vst) * C::stage, PANEL);
 #pragma unroll
         for (int k = 0; k < KT / 16; ++k)
-          mma_ts(tmem + C::o_col + x * D, tmem + 128 * u + 8 * k, desc(b + 2048 * k, PANEL), idesc(128, D, 1),
+          mma_ts(tmem + C::o_col + x * D, tmem + 128 * u + 8 * k, desc(b + (2048 >> 4) * k), idesc(128, D, 1),
                  !(first && k == 0));
         commit(bar(o_full + x));
       };
@@ -565,71 +648,60 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         tc_after();
         return true;
       };
-      bool first = true;  // of the item's products
-      uint32_t step = 0;
-      // the scores of the very first tile
-      bool ok = wait(full + kst, kph) && wait_q(0);
-      bool two = T == 2 && rows_of(wk.cur, 1) > 0;
-      if (ok) {
+      // The issuing thread must not keep the tensor core waiting: what changes from item to item
+      // is worked out between items.
+      uint32_t u = 0;  // S buffer of the step (one row tile)
+      bool ok = true;
+      while (ok && wk.more()) {
+        const int n = (int)(wk.end() - wk.w);
+        const bool two = T == 2 && rows_of(wk.cur, 1) > 0;
+        // the first scores of the item
+        if (!(ok = wait(full + kst, kph) && wait_q(0))) break;
         tc_after();
-        scores(0, 0);
-        if (two && (ok = wait_q(1))) scores(1, 1);
-      }
-      if (ok) {
+        scores(0, T == 2 ? 0 : u);
+        if (two) {
+          if (!(ok = wait_q(1))) break;
+          scores(1, 1);
+        }
         commit(bar(empty + kst));
         advance(kst, kph);
-      }
-      while (ok) {
-        Walk<TYPE, D> nx = wk;
-        const bool new_item = nx.next(p), more = nx.w < nx.w1;
-        const bool two_next = T == 2 && rows_of(nx.cur, 1) > 0;
-        if (T == 2) {
-          // product and next scores of one tile, then of the other; between items both products first
-          if (!(ok = wait(full + NS + vst, vph) && wait_p(0))) break;
-          product(0, 0, first);
-          if (more && !new_item) {
-            if (!(ok = wait(full + kst, kph))) break;
-            tc_after();
-            scores(0, 0);
+        for (int j = 0; j < n; ++j) {
+          const bool more = j + 1 < n;
+          if (T == 2) {  // product and next scores of one row tile, then of the other
+            if (!(ok = wait(full + NS + vst, vph) && wait_p(0))) break;
+            product(0, 0, j == 0);
+            if (more) {
+              if (!(ok = wait(full + kst, kph))) break;
+              tc_after();
+              scores(0, 0);
+            }
+            if (two) {
+              if (!(ok = wait_p(1))) break;
+              product(1, 1, j == 0);
+            }
+            commit(bar(empty + NS + vst));
+            advance(vst, vph);
+            if (more) {
+              if (two) scores(1, 1);
+              commit(bar(empty + kst));
+              advance(kst, kph);
+            }
+          } else {  // the next scores are formed during the softmax
+            if (more) {
+              if (!(ok = wait(full + kst, kph))) break;
+              tc_after();
+              scores(0, u ^ 1);
+              commit(bar(empty + kst));
+              advance(kst, kph);
+            }
+            if (!(ok = wait(full + NS + vst, vph) && wait_p(u))) break;
+            product(0, u, j == 0);
+            commit(bar(empty + NS + vst));
+            advance(vst, vph);
+            u ^= 1;
           }
-          if (two) {
-            if (!(ok = wait_p(1))) break;
-            product(1, 1, first);
-          }
-          commit(bar(empty + NS + vst));
-          advance(vst, vph);
-          if (!more) break;
-          if (new_item) {
-            if (!(ok = wait(full + kst, kph) && wait_q(0))) break;
-            tc_after();
-            scores(0, 0);
-            if (two_next && !(ok = wait_q(1))) break;
-          }
-          if (two_next) scores(1, 1);
-          commit(bar(empty + kst));
-          advance(kst, kph);
-        } else {
-          const int u = step & 1;
-          auto next_scores = [&]() {
-            if (!wait(full + kst, kph) || (new_item && !wait_q(0))) return false;
-            tc_after();
-            scores(0, u ^ 1);
-            commit(bar(empty + kst));
-            advance(kst, kph);
-            return true;
-          };
-          if (more && !new_item && !(ok = next_scores())) break;
-          if (!(ok = wait(full + NS + vst, vph) && wait_p(u))) break;
-          product(0, u, first);
-          commit(bar(empty + NS + vst));
-          advance(vst, vph);
-          if (!more) break;
-          if (new_item && !(ok = next_scores())) break;
         }
-        first = new_item;
-        two = two_next;
-        wk = nx;
-        ++step;
+        wk.next_item(p);
       }
       // every MMA issued above has completed once `done` flips
       commit(bar(done));
@@ -637,10 +709,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       }
     }
     __syncwarp();
-  } else if (!C::q) {
     // ------------------------------------------------------------------ TMA loaders: K, V
-    const int kv = warp - C::load_warp;
-    if (kv < 2) {
+    const int kv = warp - C::mma_warp - 1;
+    if (!C::q && (kv == 0 || kv == 1)) {
       const CUtensorMap* map = kv ? &tv : &tk;
       const uint32_t ring_addr = ptx::smem_u32(ring) + kv * NS * C::stage;
       const int shift = p.page_shift, ps = p.page_size, npg = KT >> shift;  // pages of a tile
@@ -650,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
 #pragma unroll
       for (int s = 0; s < NS; ++s) last_par[s] = -1;
       bool ok = true;
-      while (wk.w < wk.w1) {
+      while (wk.more()) {
         const Cursor& cur = wk.cur;
         const int t = wk.tile() * KT, tok = t + (pg << shift);
         // a page whose tokens are there and may be seen by some row
@@ -699,42 +770,36 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         }
       }
     }
-  } else if (warp >= C::load_warp) {
+  } else {
     // ------------------------------------------------------------------ decoding loaders
-    // The codes of the next tile are fetched before those of the last one are decoded.  K is
-    // one tile ahead of V, as its products are.
-    const int lt = tid - 32 * C::load_warp;  // 0..127
-    uint32_t st[2] = {0, 0}, ph[2] = {0, 0};
-    bool ok = true;
-    auto put = [&](int kv, const Raw<TYPE, D>& x) {
-      if (!wait_all(empty + kv * NS + st[kv], ph[kv] ^ 1u)) return false;
-      raw_store<TYPE, D>(ring + (kv * NS + st[kv]) * C::stage, lt, x);
+    regs_down<C::load_regs>();
+    // Four warps for K, four for V.  The page ids of a tile are fetched two tiles ahead, its
+    // codes one tile ahead, while the tile before is decoded.
+    const int lt = (tid - 32 * C::load_warp) & 127, kv = (warp - C::load_warp) >> 2;
+    const uint8_t* base = kv ? p.v : p.k;
+    const uint8_t* scales = kv ? p.vs : p.ks;
+    uint8_t* my_ring = ring + kv * NS * C::stage;
+    uint32_t st = 0, ph = 0;
+    Raw<TYPE, D> x;
+    raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, tile_pages(p, wk.cur, wk.tile() * KT, lane), base, scales, lt, x);
+    wk.next(p);
+    int pages = wk.more() ? tile_pages(p, wk.cur, wk.tile() * KT, lane) : -1;
+    for (bool last = false; !last;) {
+      if (!wait_all(empty + kv * NS + st, ph ^ 1u)) break;
+      raw_store<TYPE, D>(my_ring + st * C::stage, lt, x);
+      last = !wk.more();
+      if (!last) {
+        raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, pages, base, scales, lt, x);
+        wk.next(p);
+        if (wk.more()) pages = tile_pages(p, wk.cur, wk.tile() * KT, lane);
+      }
       fence_async();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(full + kv * NS + st[kv]));
-      if (++st[kv] == (uint32_t)NS) {
-        st[kv] = 0;
-        ph[kv] ^= 1u;
+      if (lane == 0) ptx::mbar_arrive(bar(full + kv * NS + st));
+      if (++st == (uint32_t)NS) {
+        st = 0;
+        ph ^= 1u;
       }
-      return true;
-    };
-    Raw<TYPE, D> xk, xv;
-    raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, p.k, p.ks, lt, xk);
-    raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, p.v, p.vs, lt, xv);
-    ok = put(0, xk);
-    while (ok && wk.w < wk.w1) {
-      wk.next(p);
-      const bool more = wk.w < wk.w1;
-      const int t = wk.tile() * KT;
-      if (more) raw_load<TYPE, D>(p, wk.cur, t, p.k, p.ks, lt, xk);
-      if (T == 1 && more) {  // the next scores come before the product
-        if (!(ok = put(0, xk))) break;
-        if (!(ok = put(1, xv))) break;
-      } else {
-        if (!(ok = put(1, xv))) break;
-        if (more && !(ok = put(0, xk))) break;
-      }
-      if (more) raw_load<TYPE, D>(p, wk.cur, t, p.v, p.vs, lt, xv);
     }
   }
   __syncwarp();

@@ -30,6 +30,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int RB = 16;             // rows of a block
 constexpr int CHUNK = 16;          // tokens of a warp's step
 constexpr int UT = CHUNK * kWarps; // tokens of a tile
+constexpr int OV = 4;              // counts of an item besides its tiles
 constexpr float kSlack = 8.f;      // log2 units by which scores may pass the running maximum
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
   float* join_o = reinterpret_cast<float*>(body);                            // [kWarps][RB][opitch]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  Cursor cur;
-  long long w, w1, per;
-  if (!plan<RB, UT, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), cur, w, w1, per)) return;
+  Walk<RB, UT, OV> wk;
+  long long per;
+  if (!plan<RB, UT, OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), 1, wk, per)) return;
   __syncthreads();
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;
@@ -189,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
 
   for (;;) {
     // ---------------------------------------------------- this CTA's part of the item
-    const int ta = (int)(w - cur.start);
-    const int tb = (int)min((long long)cur.cost, w1 - cur.start);
+    const Cursor& cur = wk.cur;
+    const int ta = (int)(wk.w - cur.start), tb = (int)(wk.end() - cur.start);
     const int rows = min(cur.n * p.group - cur.rb * RB, RB);
     {  // query operands in the order in which the keys' words hold their elements
       for (int i = tid; i < KS * 32; i += kThreads) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
           const int r = gg + 8 * (q & 1), kh = q >> 1;
           uint32_t v = 0;
           if (r < rows) {
-            const int rr = cur.rb * RB + r, tok = rr / p.group, hd = rr - tok * p.group;
+            const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = rr - tok * p.group;
             const uint16_t* src = p.q + (long long)(cur.q0 + tok) * p.q_stride + (long long)(cur.head * p.group + hd) * D;
             if (TYPE == FT_KV_BF16) {
               v = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * cc + 8 * kh));
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       const int r = g + 8 * h;
       lo[h] = hi[h] = 0;
       if (r < rows) {
-        const int pos = cur.len - cur.n + (cur.rb * RB + r) / p.group;
+        const int pos = cur.len - cur.n + div_group(p, cur.rb * RB + r);
         hi[h] = p.causal ? min(cur.len, pos + 1) : cur.len;
         lo[h] = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
       }
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       }
     }
     if (write && r < rows) {
-      const int rr = cur.rb * RB + r, tok = rr / p.group, hd = cur.head * p.group + rr - tok * p.group;
+      const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
       const float inv = ll == 0.f ? 0.f : left_in(TYPE) / ll;
       uint16_t* dst = p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D;
 #pragma unroll
@@ -533,9 +534,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       if (p.lse && sub == 0)
         p.lse[(long long)(cur.q0 + tok) * p.n_heads + hd] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
     }
-    w = cur.start + tb;
-    if (w >= w1) break;
-    cursor_next<RB, UT>(p, cur);
+    wk.next_item(p);
+    if (!wk.more()) break;
     __syncthreads();  // the ring and the join buffers are free again
   }
 }

@@ -40,7 +40,8 @@ struct AttnParams {
   const uint8_t* ks;
   const uint8_t* vs;
   int n_pages, page_size, page_shift, n_kv_heads;
-  int n_heads, group;  // group = n_heads / n_kv_heads
+  int n_heads, group;    // group = n_heads / n_kv_heads
+  uint32_t group_magic;  // ceil(2^32 / group), for group > 1
   int n_tokens, n_seqs, table_stride, causal, window;
   float scale_log2;  // scale * log2(e)
   const uint16_t* q;
@@ -59,22 +60,35 @@ struct AttnParams {
 constexpr int kMaxCtas = 4096;                     // CTAs of one attention launch, at most
 constexpr size_t kCounterBytes = kMaxCtas * 4;
 constexpr int kMaxSeqs = 1024;                     // sequences of one call
+constexpr int kMaxRows = 1 << 25;                  // rows of one cache head in one call
+
+// r / group for r < kMaxRows: with m = ceil(2^32 / g) = (2^32 + e) / g, e < g <= 128,
+// r * m / 2^32 = r / g + r * e / (g * 2^32), and the second term is below 1 / g.
+__device__ __forceinline__ int div_group(const AttnParams& p, int r) {
+  return p.group == 1 ? r : (int)__umulhi((uint32_t)r, p.group_magic);
+}
+
+// a / b, in 32 bits where both fit.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // How the work is cut.  The rows of one cache head of a sequence (row r: new token r / group,
 // query head r % group of the head's group) form blocks of RB rows.  An item is a block of
 // one head over the tiles (UT cached tokens) that its rows may see; items are ordered by
-// sequence, block and head, and every CTA takes the same number of consecutive tiles.  So
-// every CTA has the same work whatever the lengths, an item whose tiles fall to several CTAs
-// leaves one partial result in each (sums without their normalisation, and the maximum they
-// refer to), and the CTA that finishes last joins them in order.  Each CTA has at most two
-// such items, one that began before it (partial slot 2 * cta) and one that goes on after it
+// sequence, block and head.  An item counts its tiles and OV more for what it costs to begin
+// and end it, and every CTA takes the same share of consecutive counts.  So every CTA has
+// about the same work whatever the lengths, an item whose tiles fall to several CTAs leaves
+// one partial result in each (sums without their normalisation, and the maximum they refer
+// to), and the CTA that finishes last joins them in order.  Each CTA has at most two such
+// items, one that began before it (partial slot 2 * cta) and one that goes on after it
 // (2 * cta + 1).
 struct Cursor {
   int seq, rb, head;
   int q0, n, len, nb;  // of the sequence: first row of q, new tokens, cached length, row blocks
   int lo, hi;          // cached tokens that any row of the block may see
   int t0, cost;        // the block's first tile, and its tiles (at least 1)
-  long long start;     // position of the item's first tile in the order of all tiles
+  long long start;     // position of the item's first tile in the order of all counts
 };
 
 __device__ __forceinline__ void seq_range(const AttnParams& p, int s, int& q0, int& n, int& len, bool& bad) {
@@ -89,7 +103,7 @@ __device__ __forceinline__ void seq_range(const AttnParams& p, int s, int& q0, i
 // Row blocks of a sequence with n new tokens.
 template <int RB>
 __device__ __forceinline__ int row_blocks(int n, int group) {
-  return (int)(((long long)n * group + RB - 1) / RB);
+  return (n * group + RB - 1) / RB;
 }
 
 // The cached tokens that rows [rb * RB, ...) of the sequence may see, in tiles of UT tokens.
@@ -97,7 +111,7 @@ template <int RB, int UT>
 __device__ __forceinline__ void block_range(const AttnParams& p, int rb, int n, int len, int& lo, int& hi, int& t0,
                                             int& cost) {
   const int rows = n * p.group, r0 = rb * RB, r1 = min(rows, r0 + RB) - 1;
-  const int p0 = len - n + r0 / p.group, p1 = len - n + r1 / p.group;
+  const int p0 = len - n + div_group(p, r0), p1 = len - n + div_group(p, r1);
   hi = p.causal ? min(len, p1 + 1) : len;
   hi = max(hi, 0);
   lo = p.window > 0 ? min(max(p0 - p.window + 1, 0), hi) : 0;
@@ -113,9 +127,9 @@ __device__ __forceinline__ void cursor_seq(const AttnParams& p, Cursor& c) {
 }
 
 // To the next item (the caller knows that there is one).
-template <int RB, int UT>
+template <int RB, int UT, int OV>
 __device__ __forceinline__ void cursor_next(const AttnParams& p, Cursor& c) {
-  c.start += c.cost;
+  c.start += c.cost + OV;
   if (++c.head < p.n_kv_heads) return;
   c.head = 0;
   if (++c.rb == c.nb) {
@@ -128,23 +142,51 @@ __device__ __forceinline__ void cursor_next(const AttnParams& p, Cursor& c) {
   block_range<RB, UT>(p, c.rb, c.n, c.len, c.lo, c.hi, c.t0, c.cost);
 }
 
-struct PlanSmem {
-  long long sum[kMaxSeqs];  // tiles of a sequence's blocks (one head), then their prefix sums
-  long long part[32];
+// A position in a CTA's share: count w of item cur, up to w1.
+template <int RB, int UT, int OV>
+struct Walk {
   Cursor cur;
-  long long total;
-  int found;
+  long long w, w1;
+  __device__ __forceinline__ int tile() const { return cur.t0 + (int)(w - cur.start); }
+  __device__ __forceinline__ bool more() const { return w < w1; }
+  // Where this CTA's part of the item ends.
+  __device__ __forceinline__ long long end() const { return min(cur.start + cur.cost, w1); }
+  // From the end of the CTA's part of an item to its next item, if there is one.
+  __device__ __forceinline__ void next_item(const AttnParams& p) {
+    if (cur.start + cur.cost + OV >= w1) {
+      w = w1;
+    } else {
+      cursor_next<RB, UT, OV>(p, cur);
+      w = cur.start;
+    }
+  }
+  // To the next tile; true when it is one of another item.
+  __device__ __forceinline__ bool next(const AttnParams& p) {
+    if (++w < end()) return false;
+    next_item(p);
+    return true;
+  }
 };
 
-// All NT threads of the block (a multiple of 32): the number of tiles per CTA, and the item
-// that contains the CTA's first tile.  Returns false for a CTA without work.  Costs are
-// counted per head and multiplied at the end.
-template <int RB, int UT, int NT>
-__device__ bool plan(const AttnParams& p, PlanSmem& sm, Cursor& cur, long long& w0, long long& w1, long long& per) {
+struct PlanSmem {
+  long long sum[kMaxSeqs];  // counts of a sequence's blocks (one head), then their prefix sums
+  int many[kMaxSeqs];       // sequences of more blocks than one thread counts
+  long long part[33];
+  Cursor cur;
+  long long total;
+  int n_many, found;
+};
+
+// All NT threads of the block (a multiple of 32) find the CTA's share and its first item.
+// per: counts of a share, at least `least`.  Returns false for a CTA without work.  Counts are
+// summed for one head and multiplied by the heads at the end.
+template <int RB, int UT, int OV, int NT>
+__device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, OV>& wk, long long& per) {
   constexpr int kFew = 4;  // blocks of a sequence that one thread counts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sm.n_many = 0;
+  __syncthreads();
   bool any_bad = false;
-  int many = 0;
   for (int s = tid; s < p.n_seqs; s += NT) {
     int q0, n, len;
     bool bad;
@@ -156,39 +198,39 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, Cursor& cur, long long& 
       for (int b = 0; b < nb; ++b) {
         int lo, hi, t0, cost;
         block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
-        sum += cost;
+        sum += cost + OV;
       }
     } else {
-      sum = -1;
-      many = 1;
+      sm.many[atomicAdd(&sm.n_many, 1)] = s;
     }
     sm.sum[s] = sum;
   }
   if (any_bad && blockIdx.x == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
-  if (tid == 0) sm.found = -1;
-  many = __syncthreads_or(many);
-  // sequences of many blocks: a warp counts each
-  if (many) {
-    for (int s = warp; s < p.n_seqs; s += NT / 32) {
-      if (sm.sum[s] >= 0) continue;
+  __syncthreads();
+  // sequences of many blocks: several warps count a slice of one each, or a warp several of them
+  const int n_many = sm.n_many;
+  if (n_many) {
+    constexpr int NW = NT / 32;
+    const int slices = n_many < NW ? NW / n_many : 1;
+    for (int i = warp; i < n_many * slices; i += NW) {
+      const int s = sm.many[i / slices], slice = i % slices;
       int q0, n, len;
       bool bad;
       seq_range(p, s, q0, n, len, bad);
       const int nb = row_blocks<RB>(n, p.group);
       long long sum = 0;
-      for (int b = lane; b < nb; b += 32) {
+      for (int b = lane + 32 * slice; b < nb; b += 32 * slices) {
         int lo, hi, t0, cost;
         block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
-        sum += cost;
+        sum += cost + OV;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      __syncwarp();
-      if (lane == 0) sm.sum[s] = sum;
+      if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.sum[s]), (unsigned long long)sum);
     }
     __syncthreads();
   }
-  // prefix sums over the sequences (warp 0, 32 at a time)
+  // prefix sums over the sequences
   if (warp == 0) {
     long long run = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
@@ -203,60 +245,63 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, Cursor& cur, long long& 
       if (s < p.n_seqs) sm.sum[s] = run + x - v;
       run += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) sm.total = run * p.n_kv_heads;
+    if (lane == 0) sm.total = run;
   }
   __syncthreads();
-  const long long total = sm.total;
-  per = (total + gridDim.x - 1) / gridDim.x;
-  w0 = per * blockIdx.x;
-  w1 = min(w0 + per, total);
-  if (w0 >= w1) return false;
-  // the sequence: the last one that begins at or before w0 and has any tiles
-  const long long at = w0 / p.n_kv_heads;  // in tiles of one head: inside the same block
+  const long long one_head = sm.total, total = one_head * p.n_kv_heads;
+  per = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
+  const long long w0 = per * blockIdx.x;
+  wk.w = w0;
+  wk.w1 = min(w0 + per, total);
+  if (w0 >= wk.w1) return false;
+  // the sequence whose counts hold w0, taken in counts of one head (so inside the same block)
+  const long long at = quotient(w0, p.n_kv_heads);
   for (int s = tid; s < p.n_seqs; s += NT) {
-    const long long a = sm.sum[s], b = s + 1 < p.n_seqs ? sm.sum[s + 1] : total / p.n_kv_heads;
+    const long long a = sm.sum[s], b = s + 1 < p.n_seqs ? sm.sum[s + 1] : one_head;
     if (a <= at && at < b) sm.found = s;
   }
   __syncthreads();
-  if (warp == 0) {
-    Cursor c{};
-    c.seq = sm.found;
-    cursor_seq<RB, UT>(p, c);
-    long long run = sm.sum[c.seq];
-    for (int b0 = 0; b0 < c.nb; b0 += 32) {
-      int lo = 0, hi = 0, t0 = 0, cost = 0;
-      if (b0 + lane < c.nb) block_range<RB, UT>(p, b0 + lane, c.n, c.len, lo, hi, t0, cost);
-      int x = cost;  // 32 blocks of at most 2^31 / UT tiles
+  Cursor c{};
+  c.seq = sm.found;
+  cursor_seq<RB, UT>(p, c);
+  // its blocks: each thread counts a run of them, and the one that meets w0 walks its run
+  const int each = (c.nb + NT - 1) / NT, b0 = min(tid * each, c.nb), b1 = min(b0 + each, c.nb);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    block_range<RB, UT>(p, b, c.n, c.len, c.lo, c.hi, c.t0, c.cost);
+    mine += c.cost + OV;
+  }
+  long long x = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const bool here = cost > 0 && at < run + x && at >= run + x - cost;
-      if (here) {
-        c.rb = b0 + lane;
-        c.lo = lo;
-        c.hi = hi;
-        c.t0 = t0;
-        c.cost = cost;
-        const long long first = (run + x - cost) * p.n_kv_heads;  // the block's first head
-        c.head = (int)((w0 - first) / cost);
-        c.start = first + (long long)c.head * cost;
-        sm.cur = c;
-      }
-      if (__any_sync(0xffffffffu, here)) break;
-      run += __shfl_sync(0xffffffffu, x, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm.part[warp] = x;
+  __syncthreads();
+  long long run = sm.sum[c.seq] + x - mine;
+  for (int i = 0; i < warp; ++i) run += sm.part[i];
+  if (run <= at && at < run + mine) {
+    for (c.rb = b0;; ++c.rb) {
+      block_range<RB, UT>(p, c.rb, c.n, c.len, c.lo, c.hi, c.t0, c.cost);
+      if (at < run + c.cost + OV) break;
+      run += c.cost + OV;
     }
+    const long long first = run * p.n_kv_heads;  // where the block's first head starts
+    c.head = (int)quotient(w0 - first, c.cost + OV);
+    c.start = first + (long long)c.head * (c.cost + OV);
+    sm.cur = c;
   }
   __syncthreads();
-  cur = sm.cur;
-  return true;
+  wk.cur = sm.cur;
+  if (wk.w >= wk.end()) wk.next_item(p);  // the share begins in the counts behind an item's tiles
+  return wk.more();
 }
 
 // Pieces of the item at `cur`: the CTAs that hold its first and its last tile.
 __device__ __forceinline__ void piece_owners(const Cursor& cur, long long per, int& first, int& last) {
-  first = (int)(cur.start / per);
-  last = (int)((cur.start + cur.cost - 1) / per);
+  first = (int)quotient(cur.start, per);
+  last = (int)quotient(cur.start + cur.cost - 1, per);
 }
 
 }  // namespace kv
