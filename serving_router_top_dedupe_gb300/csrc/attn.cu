@@ -6,12 +6,12 @@
 namespace ft {
 namespace kv {
 
-cudaError_t attn_rows_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s);
-cudaError_t attn_chunk_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s);
-cudaError_t attn_rows_mxfp8(const AttnParams& p, int D, int n_sm, cudaStream_t s);
-cudaError_t attn_chunk_mxfp8(const AttnParams& p, int D, int n_sm, cudaStream_t s);
-cudaError_t attn_rows_mxfp4(const AttnParams& p, int D, int n_sm, cudaStream_t s);
-cudaError_t attn_chunk_mxfp4(const AttnParams& p, int D, int n_sm, cudaStream_t s);
+cudaError_t attn_rows_bf16(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_bf16(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
+cudaError_t attn_rows_mxfp8(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_mxfp8(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
+cudaError_t attn_rows_mxfp4(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
+cudaError_t attn_chunk_mxfp4(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s);
 
 namespace {
 
@@ -120,10 +120,10 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kv::kCounterBytes + 256);
   p.error_word = a->error_word_out ? a->error_word_out : p.counters + kv::kMaxCtas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, cudaStream_t);
+  using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, int, cudaStream_t);
   static const Kernel kernels[2][3] = {{kv::attn_rows_bf16, kv::attn_rows_mxfp8, kv::attn_rows_mxfp4},
                                        {kv::attn_chunk_bf16, kv::attn_chunk_mxfp8, kv::attn_chunk_mxfp4}};
-  const bool many = (long long)a->max_new * p.group > 32;  // rows of one cache head
-  const cudaError_t e = kernels[many][c->kv_type](p, c->head_dim, n_sm, s);
+  const int rows = (int)((long long)a->max_new * p.group < 33 ? a->max_new * p.group : 33);  // of one cache head
+  const cudaError_t e = kernels[rows > 32][c->kv_type](p, c->head_dim, rows, n_sm, s);
   return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }

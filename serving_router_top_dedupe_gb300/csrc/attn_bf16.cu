@@ -4,10 +4,10 @@
 
 namespace ft {
 namespace kv {
-cudaError_t attn_rows_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s) {
-  return rows::launch_type<FT_KV_BF16>(p, D, n_sm, s);
+cudaError_t attn_rows_bf16(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s) {
+  return rows::launch_type<FT_KV_BF16>(p, D, rows, n_sm, s);
 }
-cudaError_t attn_chunk_bf16(const AttnParams& p, int D, int n_sm, cudaStream_t s) {
+cudaError_t attn_chunk_bf16(const AttnParams& p, int D, int, int n_sm, cudaStream_t s) {
   return chunk::launch_type<FT_KV_BF16>(p, D, n_sm, s);
 }
 }  // namespace kv

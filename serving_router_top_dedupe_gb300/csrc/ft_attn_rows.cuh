@@ -1,21 +1,24 @@
 // Attention of few rows over the paged cache: single tokens, a few drafted tokens, and
 // (block by block) any number of rows.
 //
-// A block is 16 rows of one cache head (the query heads of the group, times new tokens), the
-// row count of one mma.sync tile.  Each cached byte is used by 16 rows only, so reading the
-// cache bounds this kernel and its layout serves that:
+// A block is 16 or 32 rows of one cache head (the query heads of the group, times new tokens):
+// one or two row tiles of mma.sync.  Each cached byte is used by these rows only, so reading the
+// cache bounds this kernel, and next to that the decoding of quantised caches:
 //  - a warp streams 16-token chunks (cp.async into its own ring of stages, several chunks ahead)
 //    and never waits for another warp; the four warps of a CTA take the four chunks of a
 //    64-token tile, each with its own running maximum, sum and accumulators, and join at the
 //    end of the CTA's part of the item;
 //  - rows lie in shared memory with their 16-byte pieces permuted by the row, so ldmatrix reads
 //    keys and (transposed) values without bank conflicts;
-//  - MXFP8 and MXFP4 codes go from ldmatrix to BF16 operands in registers.  The order of the
-//    reduction is free, and so is the order of the value columns: keys are taken in the order
-//    in which a 32-bit word holds its codes, with the queries arranged to match, and a
-//    transposed 16-bit unit holds 2 (4) neighbouring value columns of a token, which become
-//    the operands of 2 (4) column tiles.  Decoding is then a shift, two masks and one BF16
-//    multiplication by the block's scale per two elements, with no element moved.
+//  - MXFP8 and MXFP4 codes go from ldmatrix to FP16 operands in registers, one conversion for
+//    two elements: FP16 holds every E4M3 and E2M1 number.  Their scales stay outside: a 1x32
+//    block of keys is a product of its own, added to the scores times its scale in FP32; a
+//    block of values takes probabilities times its scale.  The queries become FP16 times a
+//    power of two that brings a row's largest to 2^14 (exact for elements down to 2^-28 of it).
+//  - The order of the reduction is free, and so is the order of the value columns: keys are
+//    taken in the order in which a 32-bit word holds their codes, with the queries arranged to
+//    match, and a transposed 16-bit unit holds 2 (4) neighbouring value columns of a token,
+//    which become the operands of 2 (4) column tiles.
 // The running maximum moves only when a score passes it by 2^8 or more, so the accumulators
 // are rarely rescaled.
 #pragma once
@@ -27,9 +30,9 @@ namespace kv {
 namespace rows {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int RB = 16;             // rows of a block
 constexpr int CHUNK = 16;          // tokens of a warp's step
 constexpr int UT = CHUNK * kWarps; // tokens of a tile
+constexpr int kLeast = 2;          // counts of a CTA's share, at least
 constexpr int OV = 4;              // counts of an item besides its tiles
 constexpr float kSlack = 8.f;      // log2 units by which scores may pass the running maximum
 
@@ -112,24 +115,61 @@ __device__ __forceinline__ uint32_t multiplier(uint32_t t) {
   return mul2(t >> 1, lack);
 }
 
-template <int TYPE, int D>
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Low and high 16 bits of a word: two E4M3 codes each -> FP16 pairs.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// Byte i of a word: two E2M1 codes -> an FP16 pair.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* r) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+// Scale code b of a word, as the FP32 power of two; 255 is infinity, and the zero codes of its
+// block make it NaN.
+__device__ __forceinline__ float scale_f32(uint32_t w, int b) {
+  return __uint_as_float(((w >> (8 * b)) & 0xffu) << 23);
+}
+
+template <int TYPE, int D, int MT>
 struct Cfg {
+  static constexpr bool q = TYPE != FT_KV_BF16;
+  static constexpr int RB = 16 * MT;  // rows of a block
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
-  static constexpr int room = TYPE == FT_KV_BF16 && D == 256 ? 200 * 1024 : 100 * 1024;  // one or two CTAs per SM
+  static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;  // per SM
+  static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 68 * 1024;
   static constexpr int fit = room / (kWarps * stage);
   static constexpr int stages = fit < 8 ? fit : 8;
-  static constexpr int ctas = TYPE == FT_KV_BF16 && D == 256 ? 1 : 2;
   static constexpr int ring = kWarps * stages * stage;
   static constexpr int opitch = D + 8;  // floats of a row where the warps join
   static constexpr int join = kWarps * RB * opitch * 4;
-  static constexpr int qfrag = (D / 16) * 512;
-  static constexpr int head = 1024;  // maxima and sums where the warps join
-  static constexpr int body0 = ring > join ? ring : join;
-  static constexpr int body = body0 > (int)sizeof(PlanSmem) ? body0 : (int)sizeof(PlanSmem);
+  static constexpr int qfrag = MT * (D / 16) * 512;
+  static constexpr int head = 2048;     // maxima and sums where the warps join, and the rows' query scales
+  static constexpr int weights = 160 * ctas * RB * 4;  // of an item's parts where CTAs join (up to 160 SMs)
+  static constexpr int max0 = ring > join ? ring : join, max1 = max0 > weights ? max0 : weights;
+  static constexpr int body = max1 > (int)sizeof(PlanSmem) ? max1 : (int)sizeof(PlanSmem);
   static constexpr int smem = qfrag + head + body;
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
+  static constexpr bool q_regs = D <= 128 && MT == 1;  // the queries' operands stay in registers
 };
 
 // Column of the values that accumulator half h (columns 2c and 2c+1 of tile nt) stands for.
@@ -140,109 +180,67 @@ __device__ __forceinline__ int out_col(int nt, int c, int h) {
   return 32 * (nt >> 2) + 8 * c + 4 * h + (nt & 3);
 }
 
-// A warp's 16 x D accumulators into rows of shared memory.
+// A warp's 16 x D accumulators, times f, into rows of shared memory.
 template <int TYPE, int D>
-__device__ __forceinline__ void put_rows(float* dst, int pitch, const float (*o)[4], int g, int c) {
+__device__ __forceinline__ void put_rows(float* dst, int pitch, const float (*o)[4], float f, int g, int c) {
 #pragma unroll
   for (int hr = 0; hr < 2; ++hr) {
     float* row = dst + (g + 8 * hr) * pitch;
     if (TYPE == FT_KV_BF16) {
 #pragma unroll
       for (int nt = 0; nt < D / 8; ++nt)
-        *reinterpret_cast<float2*>(row + 8 * nt + 2 * c) = make_float2(o[nt][2 * hr], o[nt][2 * hr + 1]);
+        *reinterpret_cast<float2*>(row + 8 * nt + 2 * c) = make_float2(o[nt][2 * hr] * f, o[nt][2 * hr + 1] * f);
     } else if (TYPE == FT_KV_MXFP8) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
         *reinterpret_cast<float4*>(row + 16 * j + 4 * c) =
-            make_float4(o[2 * j][2 * hr], o[2 * j + 1][2 * hr], o[2 * j][2 * hr + 1], o[2 * j + 1][2 * hr + 1]);
+            make_float4(o[2 * j][2 * hr] * f, o[2 * j + 1][2 * hr] * f, o[2 * j][2 * hr + 1] * f, o[2 * j + 1][2 * hr + 1] * f);
     } else {
 #pragma unroll
       for (int j = 0; j < D / 32; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           *reinterpret_cast<float4*>(row + 32 * j + 8 * c + 4 * h) =
-              make_float4(o[4 * j][2 * hr + h], o[4 * j + 1][2 * hr + h], o[4 * j + 2][2 * hr + h], o[4 * j + 3][2 * hr + h]);
+              make_float4(o[4 * j][2 * hr + h] * f, o[4 * j + 1][2 * hr + h] * f, o[4 * j + 2][2 * hr + h] * f,
+                          o[4 * j + 3][2 * hr + h] * f);
     }
   }
 }
 
-template <int TYPE, int D>
-__global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kernel(const AttnParams p) {
-  using C = Cfg<TYPE, D>;
-  constexpr int NT = D / 8, KS = D / 16, S = C::stages;
+template <int TYPE, int D, int MT>
+__global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_kernel(const AttnParams p) {
+  using C = Cfg<TYPE, D, MT>;
+  constexpr int NT = D / 8, KS = D / 16, S = C::stages, RB = C::RB, NB = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4* qf = reinterpret_cast<uint4*>(smem);                                // [KS][32] query operands
-  float* join_m = reinterpret_cast<float*>(smem + C::qfrag);                 // [kWarps][RB]
-  float* join_l = join_m + kWarps * RB;                                      // [kWarps][RB]
-  int* s_flag = reinterpret_cast<int*>(join_l + kWarps * RB);
+  uint4* qf = reinterpret_cast<uint4*>(smem);                 // [MT][KS][32] query operands
+  float* join_m = reinterpret_cast<float*>(smem + C::qfrag);  // [kWarps][RB]
+  float* join_l = join_m + kWarps * RB;                       // [kWarps][RB]
+  float* q_scale = join_l + kWarps * RB;                      // [RB] scale of a row's scores
+  float* row_m = q_scale + RB;                                // [RB] where CTAs join
+  float* row_l = row_m + RB;                                  // [RB]
+  int* s_flag = reinterpret_cast<int*>(row_l + RB);
   uint8_t* body = smem + C::qfrag + C::head;
-  float* join_o = reinterpret_cast<float*>(body);                            // [kWarps][RB][opitch]
+  float* join_o = reinterpret_cast<float*>(body);             // [kWarps][RB][opitch]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  Walk<RB, UT, OV> wk;
+  Walk<C::RB, UT, OV> wk;
   long long per;
-  if (!plan<RB, UT, OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), 1, wk, per)) return;
+  if (!plan<C::RB, UT, OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), kLeast, wk, per)) return;
   __syncthreads();
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;
   uint8_t* ring_g = body + warp * S * C::stage;
-  const float scale = p.scale_log2 * left_in(TYPE);
 
   for (;;) {
     // ---------------------------------------------------- this CTA's part of the item
     const Cursor& cur = wk.cur;
     const int ta = (int)(wk.w - cur.start), tb = (int)(wk.end() - cur.start);
     const int rows = min(cur.n * p.group - cur.rb * RB, RB);
-    {  // query operands in the order in which the keys' words hold their elements
-      for (int i = tid; i < KS * 32; i += kThreads) {
-        const int ks = i >> 5, l = i & 31, gg = l >> 2, cc = l & 3;
-        uint32_t a[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = gg + 8 * (q & 1), kh = q >> 1;
-          uint32_t v = 0;
-          if (r < rows) {
-            const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = rr - tok * p.group;
-            const uint16_t* src = p.q + (long long)(cur.q0 + tok) * p.q_stride + (long long)(cur.head * p.group + hd) * D;
-            if (TYPE == FT_KV_BF16) {
-              v = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * cc + 8 * kh));
-            } else if (TYPE == FT_KV_MXFP8) {
-              v = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 4 * cc + 2 * kh));
-            } else {
-              const int d = 32 * (ks >> 1) + 8 * cc + 2 * (ks & 1) + kh;
-              v = (uint32_t)__ldg(src + d) | ((uint32_t)__ldg(src + d + 4) << 16);
-            }
-          }
-          a[q] = v;
-        }
-        qf[i] = make_uint4(a[0], a[1], a[2], a[3]);
-      }
-    }
-    __syncthreads();
-    // the cached tokens that this thread's rows g and g + 8 see: [lo, hi)
-    int lo[2], hi[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g + 8 * h;
-      lo[h] = hi[h] = 0;
-      if (r < rows) {
-        const int pos = cur.len - cur.n + div_group(p, cur.rb * RB + r);
-        hi[h] = p.causal ? min(cur.len, pos + 1) : cur.len;
-        lo[h] = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-      }
-    }
-    uint32_t qr[KS][4];
-    if (D <= 128) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<uint4*>(qr[ks]) = qf[ks * 32 + lane];
-    }
-    float o[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
+    auto q_row = [&](int r) {
+      const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = rr - tok * p.group;
+      return p.q + (long long)(cur.q0 + tok) * p.q_stride + (long long)(cur.head * p.group + hd) * D;
+    };
+    // the first chunks are on their way while the queries are arranged
     const int n = tb - ta;
     const int32_t* table = p.page_table + (long long)cur.seq * p.table_stride;
     const int tok0 = (cur.t0 + ta) * UT + warp * CHUNK;  // the warp's first chunk
@@ -268,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
           cp_async16(dst + piece<C::rby>(r, pc), ksrc + u * 16, there);
           cp_async16(dst + C::kv_bytes + piece<C::rby>(r, pc), vsrc + u * 16, there);
         }
-        if constexpr (TYPE != FT_KV_BF16) {  // scales of all 16 rows
+        if constexpr (C::q) {  // scales of all 16 rows
           constexpr int PS = CHUNK * C::sby / 16;
           if (lane < 2 * PS) {
             const int i = lane % PS;
@@ -281,6 +279,91 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
     };
 #pragma unroll 1
     for (int k = 0; k < S - 1; ++k) issue(k);
+
+    if (C::q) {  // the power of two that brings a row's largest query element to 2^14
+      constexpr int TPR = kThreads / RB;  // threads of a row
+      const int r = tid / TPR, sub = tid % TPR;
+      uint32_t top = 0;
+      if (r < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(q_row(r));
+#pragma unroll
+        for (int i = sub; i < D / 8; i += TPR) {
+          const uint4 v = __ldg(src + i);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+      }
+      top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+      for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // exponent of the power: 14 - (e - 127), within what an FP32 number can be; NaN and infinity stay
+      const int k = top >= 0x7f80u || top < 0x80u ? 0 : 141 - (int)(top >> 7);
+      if (sub == 0) q_scale[r] = __uint_as_float((uint32_t)(127 + min(k, 126)) << 23);
+      __syncthreads();
+    }
+    for (int i = tid; i < MT * KS * 32; i += kThreads) {
+      const int ks = (i >> 5) % KS, mt = i / (KS * 32), l = i & 31, gg = l >> 2, cc = l & 3;
+      uint32_t a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 16 * mt + gg + 8 * (q & 1), kh = q >> 1;
+        const int d = TYPE == FT_KV_BF16 ? 16 * ks + 2 * cc + 8 * kh : TYPE == FT_KV_MXFP8 ? 16 * ks + 4 * cc + 2 * kh
+                                                              : 32 * (ks >> 1) + 8 * cc + 4 * (ks & 1) + 2 * kh;
+        uint32_t v = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(q_row(r) + d)) : 0u;
+        if (C::q) v = pack_f16(__uint_as_float(v << 16) * q_scale[r], __uint_as_float(v & 0xffff0000u) * q_scale[r]);
+        a[q] = v;
+      }
+      qf[i] = make_uint4(a[0], a[1], a[2], a[3]);
+    }
+    __syncthreads();
+    // the cached tokens that this thread's rows g and g + 8 of a row tile see: [lo, hi)
+    int lo[MT][2], hi[MT][2];
+    float scale[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 16 * mt + g + 8 * h;
+        lo[mt][h] = hi[mt][h] = 0;
+        scale[mt][h] = C::q ? p.scale_log2 / q_scale[r] : p.scale_log2;
+        if (r < rows) {
+          const int pos = cur.len - cur.n + div_group(p, cur.rb * RB + r);
+          hi[mt][h] = p.causal ? min(cur.len, pos + 1) : cur.len;
+          lo[mt][h] = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+        }
+      }
+    // what every row of the block sees: chunks inside need no mask
+    const int pos0 = cur.len - cur.n + div_group(p, cur.rb * RB);
+    const int pos1 = cur.len - cur.n + div_group(p, cur.rb * RB + rows - 1);
+    const int all_hi = p.causal ? min(cur.len, pos0 + 1) : cur.len, all_lo = p.window > 0 ? max(pos1 - p.window + 1, 0) : 0;
+
+    uint32_t qr[KS][4];
+    if (C::q_regs) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<uint4*>(qr[ks]) = qf[ks * 32 + lane];
+    }
+    auto query = [&](int mt, int ks, uint32_t* a) {
+      if (C::q_regs) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] = qr[ks][q];
+      } else {
+        *reinterpret_cast<uint4*>(a) = qf[(mt * KS + ks) * 32 + lane];
+      }
+    };
+    float o[MT][NT][4];
+    float m[MT][2], l[MT][2];
+    // Quantised values: o is relative to 2^(m + ev), l to 2^m: ev follows the largest scale of
+    // the values, so that probabilities times scales stay below 2^14 in FP16.
+    float ev = C::q ? -1000.f : 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[mt][i][j] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
 #pragma unroll 1
     for (int k = 0; k < n; ++k) {
       __syncwarp();  // every lane is done with the stage that is filled next
@@ -291,152 +374,227 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       const int t = tok0 + k * UT;
       const uint32_t st = ring + (uint32_t)(k % S) * C::stage;
       uint8_t* sc_g = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
-      if (TYPE != FT_KV_BF16 && (t < cur.lo || t + CHUNK > cur.hi)) {
+      if (C::q && (t < cur.lo || t + CHUNK > cur.hi)) {
         // rows left out: their values are zero codes, and a scale that stands for NaN would show
         if (lane < CHUNK && (t + lane < cur.lo || t + lane >= cur.hi))
           for (int i = 0; i < C::sby; ++i) sc_g[CHUNK * C::sby + lane * C::sby + i] = 0;
         __syncwarp();
       }
+      // scale codes of this thread's tokens 2c, 2c+1, 2c+8, 2c+9
+      auto scales_of = [&](const uint8_t* base, uint32_t (*w)[NB > 4 ? 2 : 1]) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint8_t* src = base + (2 * c + (x & 1) + 8 * (x >> 1)) * NB;
+          if constexpr (NB == 2) {
+            w[x][0] = *reinterpret_cast<const uint16_t*>(src);
+          } else if constexpr (NB == 4) {
+            w[x][0] = *reinterpret_cast<const uint32_t*>(src);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            w[x][0] = v.x;
+            w[x][NB > 4 ? 1 : 0] = v.y;
+          }
+        }
+      };
       // ------------------------------------------------------------ scores
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] = 0.f;
       const int mrow = (lane & 7) + ((lane >> 4) << 3), mpc = (lane >> 3) & 1;  // ldmatrix row and piece of this lane
-      if (TYPE == FT_KV_BF16) {
+      if constexpr (!C::q) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b[4];
+          uint32_t b[4], a[4];
           ldm4(b, st + piece<C::rby>(mrow, 2 * ks + mpc));
-          uint32_t a[4];
-          if (D <= 128) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a[q] = qr[ks][q];
-          } else {
-            *reinterpret_cast<uint4*>(a) = qf[ks * 32 + lane];
+          for (int mt = 0; mt < MT; ++mt) {
+            query(mt, ks, a);
+            mma(s[mt][0], a, b[0], b[1]);
+            mma(s[mt][1], a, b[2], b[3]);
           }
-          mma(s[0], a, b[0], b[1]);
-          mma(s[1], a, b[2], b[3]);
         }
       } else {
-        // scales of tokens g and g + 8, for every 1x32 block
-        const uint8_t* ks_g = sc_g;
-        constexpr int NB = D / 32, SUB = TYPE == FT_KV_MXFP8 ? 2 : 4;  // ldmatrix pieces of a block: 2 or 1
+        uint32_t kw[4][NB > 4 ? 2 : 1];
+        scales_of(sc_g, kw);
 #pragma unroll
-        for (int pb = 0; pb < D * (TYPE == FT_KV_MXFP8 ? 1 : 0) / 32 + (TYPE == FT_KV_MXFP4 ? D / 64 : 0); ++pb) {
-          uint32_t b[4];  // (tokens 0-7, piece 2pb), (0-7, 2pb+1), (8-15, 2pb), (8-15, 2pb+1)
-          ldm4(b, st + piece<C::rby>(mrow, 2 * pb + mpc));
+        for (int blk = 0; blk < NB; ++blk) {  // a 1x32 block: two k steps
+          uint32_t f[2][2][2];                // [k step][column tile] operands
+          uint32_t b[4];
+          if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (0-7, 2blk+1), (8-15, 2blk), (8-15, 2blk+1)
+            ldm4(b, st + piece<C::rby>(mrow, 2 * blk + mpc));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // piece 2pb + h
-            const int pcs = 2 * pb + h;
-            const int blk = TYPE == FT_KV_MXFP8 ? pcs / 2 : pcs;
-            const uint32_t m0 = multiplier<TYPE>((uint32_t)ks_g[g * NB + blk] * 0x01000100u);
-            const uint32_t m1 = multiplier<TYPE>((uint32_t)ks_g[(g + 8) * NB + blk] * 0x01000100u);
-            constexpr int STEPS = SUB / 2;  // k steps of one piece
+            for (int x = 0; x < 4; ++x) e4m3x4_f16(b[x], f[x & 1][x >> 1][0], f[x & 1][x >> 1][1]);
+          } else {                    // piece blk of tokens 0-7 and 8-15
+            const uint32_t at = st + piece<C::rby>(lane & 15, blk);
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(at) : "memory");
 #pragma unroll
-            for (int sp = 0; sp < STEPS; ++sp) {
-              const int ks = pcs * STEPS + sp;
-              uint32_t a[4];
-              if (D <= 128) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) a[q] = qr[ks][q];
-              } else {
-                *reinterpret_cast<uint4*>(a) = qf[ks * 32 + lane];
-              }
-#pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                const uint32_t x = b[2 * nt + h], mm = nt ? m1 : m0;
-                uint32_t b0, b1;
-                if (TYPE == FT_KV_MXFP8) {
-                  b0 = e4m3_bits(__byte_perm(x, 0, 0x1404));  // bytes 0, 1 into the high bytes of the halves
-                  b1 = e4m3_bits(__byte_perm(x, 0, 0x3424));
-                } else {
-                  b0 = sp == 0 ? e2m1_bits<0>(x) : e2m1_bits<2>(x);
-                  b1 = sp == 0 ? e2m1_bits<1>(x) : e2m1_bits<3>(x);
-                }
-                mma(s[nt], a, mul2(b0, mm), mul2(b1, mm));
-              }
+            for (int nt = 0; nt < 2; ++nt) {
+              uint32_t e[4];
+              e2m1x8_f16(b[nt], e);
+              f[0][nt][0] = e[0];
+              f[0][nt][1] = e[1];
+              f[1][nt][0] = e[2];
+              f[1][nt][1] = e[3];
             }
+          }
+          float sc[4];  // of the block, for the columns 2c, 2c+1 of both column tiles
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[x] = scale_f32(kw[x][blk >> 2], blk & 3);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int sp = 0; sp < 2; ++sp) {
+              uint32_t a[4];
+              query(mt, 2 * blk + sp, a);
+              mma_f16(acc[0], a, f[sp][0][0], f[sp][0][1]);
+              mma_f16(acc[1], a, f[sp][1][0], f[sp][1][1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s[mt][nt][q] = fmaf(acc[nt][q], sc[2 * nt + (q & 1)], s[mt][nt][q]);
           }
         }
       }
       // ------------------------------------------------------------ softmax
+      const bool inside = t >= all_lo && t + CHUNK <= all_hi;
+      float mx[MT][2];
+      bool move = false;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j = t + 8 * nt + 2 * c + (q & 1), h = q >> 1;
-          s[nt][q] = j >= lo[h] && j < hi[h] ? s[nt][q] * scale : -INFINITY;
+        for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] *= scale[mt][(i >> 1) & 1];
+        if (!inside) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = t + 8 * (i >> 2) + 2 * c + (i & 1), h = (i >> 1) & 1;
+            if (j < lo[mt][h] || j >= hi[mt][h]) s[mt][i >> 2][i & 3] = -INFINITY;
+          }
         }
-      float mx[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-      }
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
-        float al[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(m[h], mx[h]);
-          al[h] = mn == -INFINITY ? 1.f : ex2(m[h] - mn);
-          l[h] *= al[h];
-          m[h] = mn;
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= al[0];
-          o[i][1] *= al[0];
-          o[i][2] *= al[1];
-          o[i][3] *= al[1];
+          mx[mt][h] = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+          move |= mx[mt][h] > m[mt][h] + kSlack;
         }
       }
-      uint32_t pa[4];
+      uint32_t vw[4][NB > 4 ? 2 : 1];
+      float ve = 0.f;
+      if (C::q) {  // log2 of the largest scale of the chunk's values, 13 at most (255: a NaN block)
+        scales_of(sc_g + CHUNK * C::sby, vw);
+        uint32_t top = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float mu = m[h] == -INFINITY ? 0.f : m[h];
-        const float p0 = ex2(s[0][2 * h] - mu), p1 = ex2(s[0][2 * h + 1] - mu);
-        const float p2 = ex2(s[1][2 * h] - mu), p3 = ex2(s[1][2 * h + 1] - mu);
-        l[h] += (p0 + p1) + (p2 + p3);
-        pa[h] = pack(p0, p1);
-        pa[2 + h] = pack(p2, p3);
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < (NB > 4 ? 2 : 1); ++y) top = __vmaxu4(top, vw[x][y]);
+        top = __vmaxu4(top, top >> 16);
+        ve = fminf((float)max(top & 0xffu, (top >> 8) & 0xffu) - 127.f, 13.f);
+        move |= ve > ev + 6.f;
       }
+      if (__any_sync(0xffffffffu, move)) {
+        if (C::q) {
+          ve = fmaxf(ve, __shfl_xor_sync(0xffffffffu, ve, 1));
+          ve = fmaxf(ve, __shfl_xor_sync(0xffffffffu, ve, 2));
+        }
+        const float en = C::q && ve > ev + 6.f ? ve - 2.f : ev, ea = C::q ? ex2(ev - en) : 1.f;
+        ev = en;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float al[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = mx[mt][h];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            const float mn = x > m[mt][h] + kSlack ? x : m[mt][h];
+            al[h] = mn == m[mt][h] ? 1.f : ex2(m[mt][h] - mn);
+            l[mt][h] *= al[h];
+            m[mt][h] = mn;
+            al[h] *= ea;
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o[mt][i][0] *= al[0];
+            o[mt][i][1] *= al[0];
+            o[mt][i][2] *= al[1];
+            o[mt][i][3] *= al[1];
+          }
+        }
+      }
+      const float ef = C::q ? ex2(ev) : 1.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // relative to 2^(m + ev); the sum is kept relative to 2^m
+          const float mu = (m[mt][h] == -INFINITY ? 0.f : m[mt][h]) + (C::q ? ev : 0.f);
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float e = ex2(s[mt][nt][2 * h + q] - mu);
+              s[mt][nt][2 * h + q] = e;
+              sum += e;
+            }
+          l[mt][h] = fmaf(sum, ef, l[mt][h]);
+        }
       // ------------------------------------------------------------ values
       const uint32_t vst = st + C::kv_bytes;
       const int vrow = lane & 15, vpc = lane >> 4;  // (tokens 0-7, piece j), (8-15, j), (0-7, j+1), (8-15, j+1)
-      if (TYPE == FT_KV_BF16) {
+      if constexpr (!C::q) {
+        uint32_t pa[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pa[mt][i] = pack(s[mt][i >> 1][2 * (i & 1)], s[mt][i >> 1][2 * (i & 1) + 1]);
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
           uint32_t b[4];
           ldm4t(b, vst + piece<C::rby>(vrow, 2 * j + vpc));
-          mma(o[2 * j], pa, b[0], b[1]);
-          mma(o[2 * j + 1], pa, b[2], b[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma(o[mt][2 * j], pa[mt], b[0], b[1]);
+            mma(o[mt][2 * j + 1], pa[mt], b[2], b[3]);
+          }
         }
       } else {
-        constexpr int NB = D / 32;
-        const uint8_t* vs_g = sc_g + CHUNK * C::sby;
 #pragma unroll
-        for (int pb = 0; pb < C::rby / 32; ++pb) {
+        for (int blk = 0; blk < NB; ++blk) {  // 32 columns: four column tiles with one scale for a token
+          float sc[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[x] = scale_f32(vw[x][blk >> 2], blk & 3);
+          uint32_t f[4][2];  // [column tile] operands
           uint32_t b[4];
-          ldm4t(b, vst + piece<C::rby>(vrow, 2 * pb + vpc));
+          if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (8-15, 2blk), (0-7, 2blk+1), (8-15, 2blk+1)
+            ldm4t(b, vst + piece<C::rby>(vrow, 2 * blk + vpc));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int pcs = 2 * pb + h;
-            const int blk = TYPE == FT_KV_MXFP8 ? pcs / 2 : pcs;
-            const uint32_t m0 = multiplier<TYPE>((uint32_t)vs_g[(2 * c) * NB + blk] << 8 |
-                                                 (uint32_t)vs_g[(2 * c + 1) * NB + blk] << 24);
-            const uint32_t m1 = multiplier<TYPE>((uint32_t)vs_g[(2 * c + 8) * NB + blk] << 8 |
-                                                 (uint32_t)vs_g[(2 * c + 9) * NB + blk] << 24);
-            const uint32_t x0 = b[2 * h], x1 = b[2 * h + 1];
-            if (TYPE == FT_KV_MXFP8) {
-              mma(o[2 * pcs], pa, mul2(e4m3_bits(__byte_perm(x0, 0, 0x2404)), m0),
-                  mul2(e4m3_bits(__byte_perm(x1, 0, 0x2404)), m1));
-              mma(o[2 * pcs + 1], pa, mul2(e4m3_bits(__byte_perm(x0, 0, 0x3414)), m0),
-                  mul2(e4m3_bits(__byte_perm(x1, 0, 0x3414)), m1));
-            } else {
-              mma(o[4 * pcs], pa, mul2(e2m1_bits<0>(x0), m0), mul2(e2m1_bits<0>(x1), m1));
-              mma(o[4 * pcs + 1], pa, mul2(e2m1_bits<1>(x0), m0), mul2(e2m1_bits<1>(x1), m1));
-              mma(o[4 * pcs + 2], pa, mul2(e2m1_bits<2>(x0), m0), mul2(e2m1_bits<2>(x1), m1));
-              mma(o[4 * pcs + 3], pa, mul2(e2m1_bits<3>(x0), m0), mul2(e2m1_bits<3>(x1), m1));
+            for (int x = 0; x < 4; ++x)  // bytes t0d0 t0d1 t1d0 t1d1 -> (t0d0, t1d0), (t0d1, t1d1)
+              e4m3x4_f16(__byte_perm(b[x], 0, 0x3120), f[2 * (x >> 1)][x & 1], f[2 * (x >> 1) + 1][x & 1]);
+          } else {                    // piece blk of tokens 0-7 and 8-15
+            const uint32_t at = vst + piece<C::rby>(vrow, blk);
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(at) : "memory");
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // four codes of token 0 (low half) and of token 1 -> bytes of both tokens' code i:
+              // codes 0 and 2 in the low half of y, 1 and 3 in the low half of z
+              const uint32_t y = b[x] & 0x0F0F0F0Fu, z = (b[x] >> 4) & 0x0F0F0F0Fu;
+              uint32_t e[4];
+              e2m1x8_f16(__byte_perm(y | (y >> 12), z | (z >> 12), 0x5140), e);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i][x] = e[i];
             }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t pa[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // rows g, g + 8 of tokens 0-7, then of 8-15
+              pa[i] = pack_f16(s[mt][i >> 1][2 * (i & 1)] * sc[2 * (i >> 1)], s[mt][i >> 1][2 * (i & 1) + 1] * sc[2 * (i >> 1) + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_f16(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
           }
         }
       }
@@ -445,17 +603,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
     // ---------------------------------------------------- join the four warps
     __syncthreads();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (c == 0) {
-        join_m[warp * RB + g + 8 * h] = m[h];
-        join_l[warp * RB + g + 8 * h] = l[h];
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = l[mt][h];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (c == 0) {
+          join_m[warp * RB + 16 * mt + g + 8 * h] = m[mt][h];
+          join_l[warp * RB + 16 * mt + g + 8 * h] = x;
+        }
       }
+      put_rows<TYPE, D>(join_o + (warp * RB + 16 * mt) * C::opitch, C::opitch, o[mt], C::q ? ex2(ev) : 1.f, g, c);
     }
-    put_rows<TYPE, D>(join_o + warp * RB * C::opitch, C::opitch, o, g, c);
     __syncthreads();
-    const int r = tid >> 3, sub = tid & 7;  // 16 rows x 8 threads
+    constexpr int TPR = kThreads / RB, PC = D / 4 / TPR;  // threads of a row, 16-byte pieces of a thread
+    const int r = tid / TPR, sub = tid % TPR;
     float mm = -INFINITY, ll = 0.f, wt[kWarps];
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, join_m[x * RB + r]);
@@ -464,75 +627,94 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
       wt[x] = mm == -INFINITY ? 0.f : ex2(join_m[x * RB + r] - mm);
       ll += join_l[x * RB + r] * wt[x];
     }
-    float4 acc[D / 32];
+    float4 acc[PC];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < PC; ++i) {
       acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) {
-        const float4 v = *reinterpret_cast<const float4*>(join_o + (x * RB + r) * C::opitch + 4 * (sub + 8 * i));
+        const float4 v = *reinterpret_cast<const float4*>(join_o + (x * RB + r) * C::opitch + 4 * (sub + TPR * i));
         acc[i].x += v.x * wt[x];
         acc[i].y += v.y * wt[x];
         acc[i].z += v.z * wt[x];
         acc[i].w += v.w * wt[x];
       }
     }
-    bool write = true;
+    auto put = [&](int row, int piece4, float4 v, float inv) {
+      const int rr = cur.rb * RB + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
+      *reinterpret_cast<uint2*>(p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D + 4 * piece4) =
+          make_uint2(pack(v.x * inv, v.y * inv), pack(v.z * inv, v.w * inv));
+    };
+    auto put_lse = [&](int row, float mr, float lr) {
+      if (!p.lse) return;
+      const int rr = cur.rb * RB + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
+      p.lse[(long long)(cur.q0 + tok) * p.n_heads + hd] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * 0.69314718055994530942f;
+    };
     int first, last;
     piece_owners(cur, per, first, last);
-    if (first != last) {
+    if (first == last) {
+      if (r < rows) {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+        for (int i = 0; i < PC; ++i) put(r, sub + TPR * i, acc[i], inv);
+        if (sub == 0) put_lse(r, mm, ll);
+      }
+    } else {
       const int me = blockIdx.x;
       float* slot = p.partials + (size_t)(2 * me + (me == first ? 1 : 0)) * C::slot_floats;
+      if (r < rows) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(slot + r * D + 4 * (sub + 8 * i)), acc[i]);
-      if (sub == 0) {
-        __stcg(slot + RB * D + r, mm);
-        __stcg(slot + RB * D + RB + r, ll);
+        for (int i = 0; i < PC; ++i) __stcg(reinterpret_cast<float4*>(slot + r * D + 4 * (sub + TPR * i)), acc[i]);
+        if (sub == 0) {
+          __stcg(slot + RB * D + r, mm);
+          __stcg(slot + RB * D + RB + r, ll);
+        }
       }
       __threadfence();
       __syncthreads();
       if (tid == 0) *s_flag = atomicAdd(p.counters + first, 1u) == (uint32_t)(last - first);
       __syncthreads();
-      write = *s_flag != 0;
-      if (write) {
+      if (*s_flag) {
         // the last one: join the item's parts in their order
         __threadfence();
         if (tid == 0) p.counters[first] = 0u;
         auto part = [&](int x) { return p.partials + (size_t)(2 * x + (x == first ? 1 : 0)) * C::slot_floats; };
-        mm = -INFINITY;
-        for (int x = first + sub; x <= last; x += 8) mm = fmaxf(mm, __ldcg(part(x) + RB * D + r));
+        float* weight = reinterpret_cast<float*>(body);  // [parts][RB]
+        const int np = last - first + 1;
+        if (r < rows) {
+          mm = -INFINITY;
+          for (int x = sub; x < np; x += TPR) mm = fmaxf(mm, __ldcg(part(first + x) + RB * D + r));
+        }
 #pragma unroll
-        for (int d = 1; d < 8; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        ll = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int x = first; x <= last; ++x) {
-          const float* sl = part(x);
-          const float mx = __ldcg(sl + RB * D + r), lx = __ldcg(sl + RB * D + RB + r);
-          const float wx = mm == -INFINITY ? 0.f : ex2(mx - mm);
-          ll += lx * wx;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + r * D + 4 * (sub + 8 * i)));
-            acc[i].x += v.x * wx;
-            acc[i].y += v.y * wx;
-            acc[i].z += v.z * wx;
-            acc[i].w += v.w * wx;
+        for (int d = 1; d < TPR; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        if (r < rows) {
+          for (int x = sub; x < np; x += TPR)
+            weight[x * RB + r] = mm == -INFINITY ? 0.f : ex2(__ldcg(part(first + x) + RB * D + r) - mm);
+          if (sub == 0) row_m[r] = mm;
+        }
+        __syncthreads();
+        if (tid < rows) {
+          ll = 0.f;
+          for (int x = 0; x < np; ++x) ll += __ldcg(part(first + x) + RB * (D + 1) + tid) * weight[x * RB + tid];
+          row_l[tid] = ll;
+          put_lse(tid, row_m[tid], ll);
+        }
+        __syncthreads();
+        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+          const int row = i / (D / 4);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int x = 0; x < np; ++x) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(part(first + x)) + i);
+            const float f = weight[x * RB + row];
+            v.x += u.x * f;
+            v.y += u.y * f;
+            v.z += u.z * f;
+            v.w += u.w * f;
           }
+          put(row, i % (D / 4), v, row_l[row] == 0.f ? 0.f : 1.f / row_l[row]);
         }
       }
-    }
-    if (write && r < rows) {
-      const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
-      const float inv = ll == 0.f ? 0.f : left_in(TYPE) / ll;
-      uint16_t* dst = p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        *reinterpret_cast<uint2*>(dst + 4 * (sub + 8 * i)) =
-            make_uint2(pack(acc[i].x * inv, acc[i].y * inv), pack(acc[i].z * inv, acc[i].w * inv));
-      if (p.lse && sub == 0)
-        p.lse[(long long)(cur.q0 + tok) * p.n_heads + hd] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
     }
     wk.next_item(p);
     if (!wk.more()) break;
@@ -540,18 +722,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D>::ctas)) attn_rows_kern
   }
 }
 
-template <int TYPE, int D>
+template <int TYPE, int D, int MT>
 cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
-  using C = Cfg<TYPE, D>;
-  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  using C = Cfg<TYPE, D, MT>;
+  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<TYPE, D><<<n_sm * C::ctas, kThreads, C::smem, s>>>(p);
+  const int grid = n_sm * C::ctas;
+  // an item's parts are at most all CTAs: their weights must fit where the CTAs join
+  if ((size_t)grid * C::RB * 4 > (size_t)C::body || grid > kMaxCtas) return cudaErrorInvalidConfiguration;
+  attn_rows_kernel<TYPE, D, MT><<<grid, kThreads, C::smem, s>>>(p);
   return cudaGetLastError();
 }
 
+// rows: of one cache head of a sequence, at most.
 template <int TYPE>
-cudaError_t launch_type(const AttnParams& p, int D, int n_sm, cudaStream_t s) {
-  return D == 64 ? launch<TYPE, 64>(p, n_sm, s) : D == 128 ? launch<TYPE, 128>(p, n_sm, s) : launch<TYPE, 256>(p, n_sm, s);
+cudaError_t launch_type(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s) {
+  if (D == 64) return rows <= 16 ? launch<TYPE, 64, 1>(p, n_sm, s) : launch<TYPE, 64, 2>(p, n_sm, s);
+  if (D == 128) return rows <= 16 ? launch<TYPE, 128, 1>(p, n_sm, s) : launch<TYPE, 128, 2>(p, n_sm, s);
+  return launch<TYPE, 256, 1>(p, n_sm, s);
 }
 
 }  // namespace rows
