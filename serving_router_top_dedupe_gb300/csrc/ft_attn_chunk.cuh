@@ -313,6 +313,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     *abort_flag = 0;
     ptx::mbar_fence_init();
   }
+  pdl_wait();
+  pdl_trigger();
   ChunkWalk<TYPE, D> wk;
   long long per;
   if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kLeast, wk, per)) return;
@@ -847,11 +849,10 @@ cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
     e = page_map(&tk, p.k, D, p);
     if (e == cudaSuccess) e = page_map(&tv, p.v, D, p);
   }
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_chunk_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  static std::atomic<uint64_t> ready{0};  // devices whose limit is set
+  if (e == cudaSuccess) e = raise_smem(attn_chunk_kernel<TYPE, D>, C::smem, ready);
   if (e != cudaSuccess) return e;
-  attn_chunk_kernel<TYPE, D><<<n_sm, C::threads, C::smem, s>>>(tk, tv, p);
-  return cudaGetLastError();
+  return launch_k(attn_chunk_kernel<TYPE, D>, dim3(n_sm), dim3(C::threads), C::smem, s, true, tk, tv, p);
 }
 
 template <int TYPE>

@@ -53,6 +53,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
   const uint32_t n = there ? 16u : 0u;  // 0: the 16 bytes are set to zero, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -142,12 +145,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
-// Scale code b of a word, as the FP32 power of two; 255 is infinity, and the zero codes of its
-// block make it NaN.
-__device__ __forceinline__ float scale_f32(uint32_t w, int b) {
-  return __uint_as_float(((w >> (8 * b)) & 0xffu) << 23);
-}
-
 template <int TYPE, int D, int MT>
 struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
@@ -155,8 +152,9 @@ struct Cfg {
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
+  static constexpr int scales = q ? 2 * CHUNK * (D / 32) * 4 : 0;  // a warp's chunk of scales in FP32
   static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;  // per SM
-  static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 68 * 1024;
+  static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 66 * 1024;
   static constexpr int fit = room / (kWarps * stage);
   static constexpr int stages = fit < 8 ? fit : 8;
   static constexpr int ring = kWarps * stages * stage;
@@ -164,10 +162,10 @@ struct Cfg {
   static constexpr int join = kWarps * RB * opitch * 4;
   static constexpr int qfrag = MT * (D / 16) * 512;
   static constexpr int head = 2048;     // maxima and sums where the warps join, and the rows' query scales
-  static constexpr int weights = 160 * ctas * RB * 4;  // of an item's parts where CTAs join (up to 160 SMs)
+  static constexpr int weights = 160 * ctas * RB * 8;  // and sums of an item's parts where CTAs join (up to 160 SMs)
   static constexpr int max0 = ring > join ? ring : join, max1 = max0 > weights ? max0 : weights;
   static constexpr int body = max1 > (int)sizeof(PlanSmem) ? max1 : (int)sizeof(PlanSmem);
-  static constexpr int smem = qfrag + head + body;
+  static constexpr int smem = qfrag + head + body + kWarps * scales;
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
   static constexpr bool q_regs = D <= 128 && MT == 1;  // the queries' operands stay in registers
 };
@@ -216,13 +214,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
   float* join_m = reinterpret_cast<float*>(smem + C::qfrag);  // [kWarps][RB]
   float* join_l = join_m + kWarps * RB;                       // [kWarps][RB]
   float* q_scale = join_l + kWarps * RB;                      // [RB] scale of a row's scores
-  float* row_m = q_scale + RB;                                // [RB] where CTAs join
-  float* row_l = row_m + RB;                                  // [RB]
+  float* row_l = q_scale + RB;                                // [RB] where CTAs join
   int* s_flag = reinterpret_cast<int*>(row_l + RB);
   uint8_t* body = smem + C::qfrag + C::head;
   float* join_o = reinterpret_cast<float*>(body);             // [kWarps][RB][opitch]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  pdl_wait();
+  pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
   Walk<C::RB, UT, OV> wk;
   long long per;
   if (!plan<C::RB, UT, OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), kLeast, wk, per)) return;
@@ -230,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;
   uint8_t* ring_g = body + warp * S * C::stage;
+  float* sc_f = reinterpret_cast<float*>(body + C::body + warp * C::scales);  // [K, V][CHUNK][NB]
 
   for (;;) {
     // ---------------------------------------------------- this CTA's part of the item
@@ -259,12 +259,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         const uint8_t* vsrc = p.v + row * C::rby;
         const uint32_t dst = ring + (uint32_t)(k % S) * C::stage;
         constexpr int PR = C::rby / 16;
+        if (r0 == 0 && r1 == CHUNK) {
 #pragma unroll
-        for (int i = 0; i < CHUNK * PR / 32; ++i) {
-          const int u = lane + 32 * i, r = u / PR, pc = u % PR;
-          const bool there = r >= r0 && r < r1;
-          cp_async16(dst + piece<C::rby>(r, pc), ksrc + u * 16, there);
-          cp_async16(dst + C::kv_bytes + piece<C::rby>(r, pc), vsrc + u * 16, there);
+          for (int i = 0; i < CHUNK * PR / 32; ++i) {
+            const int u = lane + 32 * i;
+            cp_async16(dst + piece<C::rby>(u / PR, u % PR), ksrc + u * 16);
+            cp_async16(dst + C::kv_bytes + piece<C::rby>(u / PR, u % PR), vsrc + u * 16);
+          }
+        } else {
+#pragma unroll 2
+          for (int i = 0; i < CHUNK * PR / 32; ++i) {
+            const int u = lane + 32 * i, r = u / PR, pc = u % PR;
+            const bool there = r >= r0 && r < r1;
+            cp_async16(dst + piece<C::rby>(r, pc), ksrc + u * 16, there);
+            cp_async16(dst + C::kv_bytes + piece<C::rby>(r, pc), vsrc + u * 16, there);
+          }
         }
         if constexpr (C::q) {  // scales of all 16 rows
           constexpr int PS = CHUNK * C::sby / 16;
@@ -373,26 +382,39 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       if (!wanted(k)) continue;
       const int t = tok0 + k * UT;
       const uint32_t st = ring + (uint32_t)(k % S) * C::stage;
-      uint8_t* sc_g = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
-      if (C::q && (t < cur.lo || t + CHUNK > cur.hi)) {
-        // rows left out: their values are zero codes, and a scale that stands for NaN would show
-        if (lane < CHUNK && (t + lane < cur.lo || t + lane >= cur.hi))
-          for (int i = 0; i < C::sby; ++i) sc_g[CHUNK * C::sby + lane * C::sby + i] = 0;
+      float ve = 0.f;
+      if constexpr (C::q) {
+        // The chunk's scale codes as FP32 powers of two (255: infinity, which makes the zero codes
+        // of its block NaN), zero for tokens that are left out; and log2 of the largest one of
+        // the values, 13 at most.
+        const uint8_t* codes = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
+        constexpr int PER = 2 * CHUNK * NB / 32;  // codes of a lane: all of K or all of V
+        uint32_t top = 0;
+        float f[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int tok = t + (lane * PER + i) % (CHUNK * NB) / NB;
+          const uint32_t code = codes[lane * PER + i];
+          const bool in = tok >= cur.lo && tok < cur.hi;
+          f[i] = __uint_as_float(in ? code << 23 : 0u);
+          top = max(top, in && code < 255u ? code : 0u);
+        }
+        top = __reduce_max_sync(0xffffffffu, lane >= 16 ? top : 0u);
+        ve = fminf((float)top - 127.f, 13.f);
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) *reinterpret_cast<float2*>(sc_f + lane * PER + i) = make_float2(f[i], f[i + 1]);
         __syncwarp();
       }
-      // scale codes of this thread's tokens 2c, 2c+1, 2c+8, 2c+9
-      auto scales_of = [&](const uint8_t* base, uint32_t (*w)[NB > 4 ? 2 : 1]) {
+      // of this thread's tokens 2c, 2c+1, 2c+8, 2c+9
+      auto scales_of = [&](const float* base, float (*w)[NB]) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint8_t* src = base + (2 * c + (x & 1) + 8 * (x >> 1)) * NB;
+          const float* src = base + (2 * c + (x & 1) + 8 * (x >> 1)) * NB;
           if constexpr (NB == 2) {
-            w[x][0] = *reinterpret_cast<const uint16_t*>(src);
-          } else if constexpr (NB == 4) {
-            w[x][0] = *reinterpret_cast<const uint32_t*>(src);
+            *reinterpret_cast<float2*>(w[x]) = *reinterpret_cast<const float2*>(src);
           } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[x][0] = v.x;
-            w[x][NB > 4 ? 1 : 0] = v.y;
+#pragma unroll
+            for (int y = 0; y < NB; y += 4) *reinterpret_cast<float4*>(w[x] + y) = *reinterpret_cast<const float4*>(src + y);
           }
         }
       };
@@ -416,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
       } else {
-        uint32_t kw[4][NB > 4 ? 2 : 1];
-        scales_of(sc_g, kw);
+        float kw[4][NB];
+        scales_of(sc_f, kw);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {  // a 1x32 block: two k steps
           uint32_t f[2][2][2];                // [k step][column tile] operands
@@ -439,9 +461,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
               f[1][nt][1] = e[3];
             }
           }
-          float sc[4];  // of the block, for the columns 2c, 2c+1 of both column tiles
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[x] = scale_f32(kw[x][blk >> 2], blk & 3);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -455,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) s[mt][nt][q] = fmaf(acc[nt][q], sc[2 * nt + (q & 1)], s[mt][nt][q]);
+              for (int q = 0; q < 4; ++q) s[mt][nt][q] = fmaf(acc[nt][q], kw[2 * nt + (q & 1)][blk], s[mt][nt][q]);
           }
         }
       }
@@ -480,24 +499,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           move |= mx[mt][h] > m[mt][h] + kSlack;
         }
       }
-      uint32_t vw[4][NB > 4 ? 2 : 1];
-      float ve = 0.f;
-      if (C::q) {  // log2 of the largest scale of the chunk's values, 13 at most (255: a NaN block)
-        scales_of(sc_g + CHUNK * C::sby, vw);
-        uint32_t top = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int y = 0; y < (NB > 4 ? 2 : 1); ++y) top = __vmaxu4(top, vw[x][y]);
-        top = __vmaxu4(top, top >> 16);
-        ve = fminf((float)max(top & 0xffu, (top >> 8) & 0xffu) - 127.f, 13.f);
-        move |= ve > ev + 6.f;
-      }
+      if (C::q) move |= ve > ev + 6.f;
       if (__any_sync(0xffffffffu, move)) {
-        if (C::q) {
-          ve = fmaxf(ve, __shfl_xor_sync(0xffffffffu, ve, 1));
-          ve = fmaxf(ve, __shfl_xor_sync(0xffffffffu, ve, 2));
-        }
         const float en = C::q && ve > ev + 6.f ? ve - 2.f : ev, ea = C::q ? ex2(ev - en) : 1.f;
         ev = en;
 #pragma unroll
@@ -561,11 +564,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
       } else {
+        float vw[4][NB];
+        scales_of(sc_f + CHUNK * NB, vw);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {  // 32 columns: four column tiles with one scale for a token
-          float sc[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[x] = scale_f32(vw[x][blk >> 2], blk & 3);
           uint32_t f[4][2];  // [column tile] operands
           uint32_t b[4];
           if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (8-15, 2blk), (0-7, 2blk+1), (8-15, 2blk+1)
@@ -592,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
             uint32_t pa[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // rows g, g + 8 of tokens 0-7, then of 8-15
-              pa[i] = pack_f16(s[mt][i >> 1][2 * (i & 1)] * sc[2 * (i >> 1)], s[mt][i >> 1][2 * (i & 1) + 1] * sc[2 * (i >> 1) + 1]);
+              pa[i] = pack_f16(s[mt][i >> 1][2 * (i & 1)] * vw[2 * (i >> 1)][blk],
+                               s[mt][i >> 1][2 * (i & 1) + 1] * vw[2 * (i >> 1) + 1][blk]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_f16(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
           }
@@ -681,38 +684,53 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         auto part = [&](int x) { return p.partials + (size_t)(2 * x + (x == first ? 1 : 0)) * C::slot_floats; };
         float* weight = reinterpret_cast<float*>(body);  // [parts][RB]
         const int np = last - first + 1;
-        if (r < rows) {
-          mm = -INFINITY;
-          for (int x = sub; x < np; x += TPR) mm = fmaxf(mm, __ldcg(part(first + x) + RB * D + r));
+        // maxima and sums of all parts, one load each; then weights in place of the maxima
+        float* part_l = weight + np * RB;
+        for (int i = tid; i < np * RB; i += kThreads) {
+          const int x = i / RB, row = i % RB;
+          weight[i] = row < rows ? __ldcg(part(first + x) + RB * D + row) : -INFINITY;
+          part_l[i] = row < rows ? __ldcg(part(first + x) + RB * (D + 1) + row) : 0.f;
         }
+        __syncthreads();
+        mm = -INFINITY;
+        ll = 0.f;
+        for (int x = sub; x < np; x += TPR) mm = fmaxf(mm, weight[x * RB + r]);
 #pragma unroll
         for (int d = 1; d < TPR; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        if (r < rows) {
-          for (int x = sub; x < np; x += TPR)
-            weight[x * RB + r] = mm == -INFINITY ? 0.f : ex2(__ldcg(part(first + x) + RB * D + r) - mm);
-          if (sub == 0) row_m[r] = mm;
+        for (int x = sub; x < np; x += TPR) {
+          const float f = mm == -INFINITY ? 0.f : ex2(weight[x * RB + r] - mm);
+          weight[x * RB + r] = f;
+          ll += part_l[x * RB + r] * f;
+        }
+#pragma unroll
+        for (int d = 1; d < TPR; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+        if (sub == 0 && r < rows) {
+          row_l[r] = ll;
+          put_lse(r, mm, ll);
         }
         __syncthreads();
-        if (tid < rows) {
-          ll = 0.f;
-          for (int x = 0; x < np; ++x) ll += __ldcg(part(first + x) + RB * (D + 1) + tid) * weight[x * RB + tid];
-          row_l[tid] = ll;
-          put_lse(tid, row_m[tid], ll);
-        }
-        __syncthreads();
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
-          const int row = i / (D / 4);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        // two 16-byte pieces of a thread at a time, the parts in their order, many loads in flight
+        const int pieces = rows * (D / 4);
+        for (int i0 = tid; i0 < pieces; i0 += 2 * kThreads) {
+          const int i1 = i0 + kThreads < pieces ? i0 + kThreads : i0;
+          const int row0 = i0 / (D / 4), row1 = i1 / (D / 4);
+          float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
 #pragma unroll 8
           for (int x = 0; x < np; ++x) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(part(first + x)) + i);
-            const float f = weight[x * RB + row];
-            v.x += u.x * f;
-            v.y += u.y * f;
-            v.z += u.z * f;
-            v.w += u.w * f;
+            const float4* src = reinterpret_cast<const float4*>(part(first + x));
+            const float4 u0 = __ldcg(src + i0), u1 = __ldcg(src + i1);
+            const float f0 = weight[x * RB + row0], f1 = weight[x * RB + row1];
+            v0.x += u0.x * f0;
+            v0.y += u0.y * f0;
+            v0.z += u0.z * f0;
+            v0.w += u0.w * f0;
+            v1.x += u1.x * f1;
+            v1.y += u1.y * f1;
+            v1.z += u1.z * f1;
+            v1.w += u1.w * f1;
           }
-          put(row, i % (D / 4), v, row_l[row] == 0.f ? 0.f : 1.f / row_l[row]);
+          put(row0, i0 % (D / 4), v0, row_l[row0] == 0.f ? 0.f : 1.f / row_l[row0]);
+          if (i1 != i0) put(row1, i1 % (D / 4), v1, row_l[row1] == 0.f ? 0.f : 1.f / row_l[row1]);
         }
       }
     }
@@ -725,13 +743,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 template <int TYPE, int D, int MT>
 cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
   using C = Cfg<TYPE, D, MT>;
-  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  static std::atomic<uint64_t> ready{0};  // devices whose limit is set
+  cudaError_t e = raise_smem(attn_rows_kernel<TYPE, D, MT>, C::smem, ready);
   if (e != cudaSuccess) return e;
   const int grid = n_sm * C::ctas;
   // an item's parts are at most all CTAs: their weights must fit where the CTAs join
-  if ((size_t)grid * C::RB * 4 > (size_t)C::body || grid > kMaxCtas) return cudaErrorInvalidConfiguration;
-  attn_rows_kernel<TYPE, D, MT><<<grid, kThreads, C::smem, s>>>(p);
-  return cudaGetLastError();
+  if ((size_t)grid * C::RB * 8 > (size_t)C::body || grid > kMaxCtas) return cudaErrorInvalidConfiguration;
+  return launch_k(attn_rows_kernel<TYPE, D, MT>, dim3(grid), dim3(kThreads), C::smem, s, true, p);
 }
 
 // rows: of one cache head of a sequence, at most.

@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ft_internal.cuh"
@@ -28,6 +29,19 @@ __host__ __device__ constexpr int scale_bytes(int type, int D) { return type == 
 __host__ __device__ constexpr float left_in(int type) { return type == FT_KV_MXFP4 ? 65536.f : 1.f; }
 
 inline int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
+// Sets a kernel's shared-memory limit on the current device, once.
+template <typename K>
+cudaError_t raise_smem(K kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit);
+  return e;
+}
 
 // Argument checks of a cache description (kv_cache.cu).
 ft_status check_cache(const char* name, const ft_kv_cache* c);
@@ -182,8 +196,79 @@ struct PlanSmem {
 // summed for one head and multiplied by the heads at the end.
 template <int RB, int UT, int OV, int NT>
 __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, OV>& wk, long long& per) {
-  constexpr int kFew = 4;  // blocks of a sequence that one thread counts
+  constexpr int kFew = 4;    // blocks of a sequence that one thread counts
+  constexpr int kStrips = 4; // sequences / 32 that a warp counts by itself
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.n_seqs <= 32 * kStrips) {
+    // Few sequences of few blocks each, as in decode: every warp counts them all, and nothing
+    // waits for another warp.
+    int sum[kStrips], q0, n, len;
+    bool alone = true, any_bad = false;
+#pragma unroll
+    for (int i = 0; i < kStrips; ++i) {
+      sum[i] = 0;
+      const int s = 32 * i + lane;
+      if (s < p.n_seqs) {
+        bool bad;
+        seq_range(p, s, q0, n, len, bad);
+        any_bad |= bad;
+        const int nb = row_blocks<RB>(n, p.group);
+        alone &= nb <= kFew;
+        for (int b = 0; b < min(nb, kFew); ++b) {
+          int lo, hi, t0, cost;
+          block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
+          sum[i] += cost + OV;
+        }
+      }
+    }
+    if (__all_sync(0xffffffffu, alone)) {
+      if (any_bad && blockIdx.x == 0 && warp == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+      long long before[kStrips], run = 0;  // counts of one head before a strip's sequences
+#pragma unroll
+      for (int i = 0; i < kStrips; ++i) {
+        if (32 * i < p.n_seqs) {
+          long long x = sum[i];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          before[i] = run + x - sum[i];
+          run += __shfl_sync(0xffffffffu, x, 31);
+        } else {
+          before[i] = run;
+        }
+      }
+      const long long total = run * p.n_kv_heads;
+      per = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
+      wk.w = per * blockIdx.x;
+      wk.w1 = min(wk.w + per, total);
+      if (wk.w >= wk.w1) return false;
+      const long long at = quotient(wk.w, p.n_kv_heads);
+      Cursor& c = wk.cur;
+      long long base = 0;
+#pragma unroll
+      for (int i = 0; i < kStrips; ++i) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, before[i] <= at && at < before[i] + sum[i]);
+        if (hit) {
+          const int from = __ffs(hit) - 1;
+          c.seq = 32 * i + from;
+          base = __shfl_sync(0xffffffffu, before[i], from);
+        }
+      }
+      cursor_seq<RB, UT>(p, c);
+      for (c.rb = 0;; ++c.rb) {
+        block_range<RB, UT>(p, c.rb, c.n, c.len, c.lo, c.hi, c.t0, c.cost);
+        if (at < base + c.cost + OV) break;
+        base += c.cost + OV;
+      }
+      const long long first = base * p.n_kv_heads;
+      c.head = (int)quotient(wk.w - first, c.cost + OV);
+      c.start = first + (long long)c.head * (c.cost + OV);
+      if (wk.w >= wk.end()) wk.next_item(p);
+      return wk.more();
+    }
+  }
   if (tid == 0) sm.n_many = 0;
   __syncthreads();
   bool any_bad = false;

@@ -156,6 +156,8 @@ __device__ __forceinline__ int slot_of(const RowsParams& p, int t) {
 template <int TYPE, int D, bool WRITE>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   constexpr int NB = D / 32;
+  pdl_wait();
+  pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int per = p.n_kv_heads * NB;
   const int t = (int)(i / per);
@@ -203,18 +205,17 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
 }
 
 template <int TYPE, int D>
-void launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
+cudaError_t launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
   const long long threads = (long long)p.n_tokens * p.n_kv_heads * (D / 32);
   const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
-  if (write) rows_kernel<TYPE, D, true><<<grid, kThreads, 0, s>>>(p);
-  else rows_kernel<TYPE, D, false><<<grid, kThreads, 0, s>>>(p);
+  return write ? launch_k(rows_kernel<TYPE, D, true>, grid, dim3(kThreads), 0, s, true, p)
+               : launch_k(rows_kernel<TYPE, D, false>, grid, dim3(kThreads), 0, s, true, p);
 }
 
 template <int TYPE>
-void launch_rows_d(int D, const RowsParams& p, bool write, cudaStream_t s) {
-  if (D == 64) launch_rows_t<TYPE, 64>(p, write, s);
-  else if (D == 128) launch_rows_t<TYPE, 128>(p, write, s);
-  else launch_rows_t<TYPE, 256>(p, write, s);
+cudaError_t launch_rows_d(int D, const RowsParams& p, bool write, cudaStream_t s) {
+  return D == 64 ? launch_rows_t<TYPE, 64>(p, write, s) : D == 128 ? launch_rows_t<TYPE, 128>(p, write, s)
+                                                                   : launch_rows_t<TYPE, 256>(p, write, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -250,10 +251,9 @@ ft_status rows_call(const char* name, const ft_kv_cache* c, int n_tokens, const 
   p.n_slots = c->n_pages * c->page_size;
   p.error_word = error_word;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (c->kv_type == FT_KV_BF16) launch_rows_d<FT_KV_BF16>(c->head_dim, p, write, s);
-  else if (c->kv_type == FT_KV_MXFP8) launch_rows_d<FT_KV_MXFP8>(c->head_dim, p, write, s);
-  else launch_rows_d<FT_KV_MXFP4>(c->head_dim, p, write, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = c->kv_type == FT_KV_BF16    ? launch_rows_d<FT_KV_BF16>(c->head_dim, p, write, s)
+                        : c->kv_type == FT_KV_MXFP8 ? launch_rows_d<FT_KV_MXFP8>(c->head_dim, p, write, s)
+                                                    : launch_rows_d<FT_KV_MXFP4>(c->head_dim, p, write, s);
   return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 

@@ -403,13 +403,13 @@ def _dense(what, t, shape, itemsize) -> None:
                          f"got {list(t.shape)} of {t.dtype}")
 
 
-def _rows(what, t, heads, dim) -> int:
-    """Token stride of [n][heads][dim] 16-bit rows that are each contiguous."""
-    if t.element_size() != 2 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (
-            t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
-        raise ValueError(f"{what}: expected rows of [{heads}][{dim}] BF16 elements, got {list(t.shape)} of {t.dtype} "
-                         f"with strides {list(t.stride())}")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+def _rows(what, t, n, heads, dim) -> int:
+    """Token stride of t, which has to be [n][heads][dim] 16-bit rows that are each contiguous."""
+    s = t.stride()
+    if t.shape != (n, heads, dim) or t.element_size() != 2 or n and (s[2] != 1 or heads > 1 and s[1] != dim):
+        raise ValueError(f"{what}: expected rows of [{n}][{heads}][{dim}] BF16 elements, got {list(t.shape)} of {t.dtype} "
+                         f"with strides {list(s)}")
+    return s[0] if n > 1 else heads * dim
 
 
 def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_scale=None, v_scale=None) -> ft_kv_cache:
@@ -429,28 +429,29 @@ def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_sca
                 raise ValueError(f"{name} is missing")
             _dense(name, t, (*lead, head_dim // 32), 1)
     c = ft_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
-    c.tensors = (k, v, k_scale, v_scale)
+    c.tensors, c.row, c.ref = (k, v, k_scale, v_scale), (n_kv_heads, head_dim), C.byref(c)
     return c
+
+
+def _kv_rows(cache, a, b, names, slots):
+    """n, strides of both tensors: the checks that ft_kv_write and ft_kv_read share."""
+    n = a.shape[0]
+    if slots.shape != (n,) or slots.element_size() != 4 or not slots.is_contiguous():
+        _dense("slots", slots, (n,), 4)
+    return n, _rows(names[0], a, n, *cache.row), _rows(names[1], b, n, *cache.row)
 
 
 def ft_kv_write(cache, k, v, slots, error_word=None, stream=None) -> None:
     """k, v: torch BF16 [n][n_kv_heads][head_dim], rows contiguous (parts of a wider tensor are fine); slots: int32 [n]."""
-    ks, vs = (_rows(w, t, cache.n_kv_heads, cache.head_dim) for w, t in (("k", k), ("v", v)))
-    _dense("slots", slots, (k.shape[0],), 4)
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
-    _check(_lib.ft_kv_write(C.byref(cache), k.shape[0], k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(),
-                            _ptr(error_word), stream))
+    n, ks, vs = _kv_rows(cache, k, v, ("k", "v"), slots)
+    _check(_lib.ft_kv_write(cache.ref, n, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), _ptr(error_word), stream))
 
 
 def ft_kv_read(cache, slots, k_out, v_out, error_word=None, stream=None) -> None:
     """The rows of `slots` as BF16 into k_out, v_out (laid out as ft_kv_write's k and v)."""
-    ks, vs = (_rows(w, t, cache.n_kv_heads, cache.head_dim) for w, t in (("k_out", k_out), ("v_out", v_out)))
-    _dense("slots", slots, (k_out.shape[0],), 4)
-    if v_out.shape[0] != k_out.shape[0]:
-        raise ValueError(f"k_out has {k_out.shape[0]} tokens, v_out {v_out.shape[0]}")
-    _check(_lib.ft_kv_read(C.byref(cache), k_out.shape[0], slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ks, vs,
-                           _ptr(error_word), stream))
+    n, ks, vs = _kv_rows(cache, k_out, v_out, ("k_out", "v_out"), slots)
+    _check(_lib.ft_kv_read(cache.ref, n, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ks, vs, _ptr(error_word),
+                           stream))
 
 
 def ft_attn_workspace(n_heads, n_kv_heads, head_dim) -> int:
@@ -465,9 +466,7 @@ def make_attn_args(n_heads, max_new, q, q_start, kv_len, page_table, out, worksp
     change.  q, out: BF16 [n_tokens][n_heads][head_dim], rows contiguous; q_start int32 [n_seqs + 1]; kv_len int32
     [n_seqs]; page_table int32 [n_seqs][pages]; lse FP32 [n_tokens][n_heads] or None."""
     n, dim = q.shape[0], q.shape[-1]
-    qs, os_ = _rows("q", q, n_heads, dim), _rows("out", out, n_heads, dim)
-    if out.shape[0] != n:
-        raise ValueError(f"q has {n} tokens, out {out.shape[0]}")
+    qs, os_ = _rows("q", q, n, n_heads, dim), _rows("out", out, n, n_heads, dim)
     seqs = kv_len.shape[0]
     _dense("kv_len", kv_len, (None,), 4)
     _dense("q_start", q_start, (seqs + 1,), 4)
@@ -477,11 +476,11 @@ def make_attn_args(n_heads, max_new, q, q_start, kv_len, page_table, out, worksp
     a = ft_attn_args(n_heads, n, seqs, max_new, page_table.shape[1], int(bool(causal)), window, scale, _ptr(q), qs,
                      _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(out), os_, _ptr(lse), _ptr(workspace),
                      workspace.numel() * workspace.element_size(), _ptr(error_word))
-    a.tensors, a.head_dim = (q, q_start, kv_len, page_table, out, workspace, lse, error_word), dim
+    a.tensors, a.head_dim, a.ref = (q, q_start, kv_len, page_table, out, workspace, lse, error_word), dim, C.byref(a)
     return a
 
 
 def ft_attn(cache, args, stream=None) -> None:
-    if args.head_dim != cache.head_dim:
-        raise ValueError(f"q has rows of {args.head_dim}, the cache of {cache.head_dim}")
-    _check(_lib.ft_attn(C.byref(cache), C.byref(args), stream))
+    if args.head_dim != cache.row[1]:
+        raise ValueError(f"q has rows of {args.head_dim}, the cache of {cache.row[1]}")
+    _check(_lib.ft_attn(cache.ref, args.ref, stream))
