@@ -4,9 +4,9 @@
 // A block is 16 or 32 rows of one cache head (the query heads of the group, times new tokens):
 // one or two row tiles of mma.sync.  Each cached byte is used by these rows only, so reading the
 // cache bounds this kernel, and next to that the decoding of quantised caches:
-//  - a warp streams 16-token chunks (cp.async into its own ring of stages, several chunks ahead)
-//    and never waits for another warp; the four warps of a CTA take the four chunks of a
-//    64-token tile, each with its own running maximum, sum and accumulators, and join at the
+//  - a warp streams chunks of 16 or 32 tokens (cp.async into its own ring of stages, several
+//    chunks ahead) and never waits for another warp; the four warps of a CTA take the four
+//    chunks of a tile, each with its own running maximum, sum and accumulators, and join at the
 //    end of the CTA's part of the item;
 //  - rows lie in shared memory with their 16-byte pieces permuted by the row, so ldmatrix reads
 //    keys and (transposed) values without bank conflicts;
@@ -30,10 +30,6 @@ namespace kv {
 namespace rows {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int CHUNK = 16;          // tokens of a warp's step
-constexpr int UT = CHUNK * kWarps; // tokens of a tile
-constexpr int kLeast = 2;          // counts of a CTA's share, at least
-constexpr int OV = 4;              // counts of an item besides its tiles
 constexpr float kSlack = 8.f;      // log2 units by which scores may pass the running maximum
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -73,6 +69,13 @@ __device__ __forceinline__ void ldm4t(uint32_t* r, uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+
+__device__ __forceinline__ void ldm2(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm2t(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
 
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -149,12 +152,18 @@ template <int TYPE, int D, int MT>
 struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
   static constexpr int RB = 16 * MT;  // rows of a block
+  // Tokens of a warp's step.  Quantised: twice as many independent products in a chain that
+  // is long for decoding; 256-wide heads have no registers for that.
+  static constexpr int CHUNK = q && D <= 128 ? 32 : 16;
+  static constexpr int UT = CHUNK * kWarps;          // tokens of a tile
+  static constexpr int OV = CHUNK == 32 ? 2 : 4;     // counts of an item besides its tiles
+  static constexpr int least = CHUNK == 32 ? 1 : 2;  // counts of a CTA's share, at least
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
   static constexpr int scales = q ? 2 * CHUNK * (D / 32) * 4 : 0;  // a warp's chunk of scales in FP32
-  static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;  // per SM
-  static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 66 * 1024;
+  static constexpr int ctas = D == 256 && !q ? 1 : 2;  // per SM
+  static constexpr int room = ctas == 1 ? 200 * 1024 : 100 * 1024;
   static constexpr int fit = room / (kWarps * stage);
   static constexpr int stages = fit < 8 ? fit : 8;
   static constexpr int ring = kWarps * stages * stage;
@@ -209,6 +218,7 @@ template <int TYPE, int D, int MT>
 __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_kernel(const AttnParams p) {
   using C = Cfg<TYPE, D, MT>;
   constexpr int NT = D / 8, KS = D / 16, S = C::stages, RB = C::RB, NB = D / 32;
+  constexpr int CHUNK = C::CHUNK, UT = C::UT, TT = CHUNK / 8;  // TT: column tiles of a chunk's scores
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* qf = reinterpret_cast<uint4*>(smem);                 // [MT][KS][32] query operands
   float* join_m = reinterpret_cast<float*>(smem + C::qfrag);  // [kWarps][RB]
@@ -222,14 +232,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
-  Walk<C::RB, UT, OV> wk;
+  Walk<RB, UT, C::OV> wk;
   long long per;
-  if (!plan<C::RB, UT, OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), kLeast, wk, per)) return;
+  if (!plan<RB, UT, C::OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), C::least, wk, per)) return;
   __syncthreads();
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;
   uint8_t* ring_g = body + warp * S * C::stage;
-  float* sc_f = reinterpret_cast<float*>(body + C::body + warp * C::scales);  // [K, V][CHUNK][NB]
+  float* sc_f = reinterpret_cast<float*>(body + C::body + warp * C::scales);  // [K, V][NB][CHUNK]
 
   for (;;) {
     // ---------------------------------------------------- this CTA's part of the item
@@ -245,42 +255,57 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
     const int32_t* table = p.page_table + (long long)cur.seq * p.table_stride;
     const int tok0 = (cur.t0 + ta) * UT + warp * CHUNK;  // the warp's first chunk
     auto wanted = [&](int k) { return k < n && tok0 + k * UT < cur.hi && tok0 + k * UT + CHUNK > cur.lo; };
-    int page_next = wanted(0) ? __ldg(table + (tok0 >> p.page_shift)) : 0;
-    auto issue = [&](int k) {
-      const int page = page_next, t = tok0 + k * UT;
-      if (wanted(k + 1)) page_next = __ldg(table + ((t + UT) >> p.page_shift));
-      if (wanted(k)) {
-        const bool ok = (unsigned)page < (unsigned)p.n_pages;
-        if (!ok && lane == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
-        const int r0 = max(cur.lo - t, 0), r1 = ok ? min(cur.hi - t, CHUNK) : 0;  // rows to read; the others are zeros
-        const long long row = (((long long)(ok ? page : 0) * p.n_kv_heads + cur.head) << p.page_shift) +
-                              (t & (p.page_size - 1));
-        const uint8_t* ksrc = p.k + row * C::rby;
-        const uint8_t* vsrc = p.v + row * C::rby;
-        const uint32_t dst = ring + (uint32_t)(k % S) * C::stage;
-        constexpr int PR = C::rby / 16;
-        if (r0 == 0 && r1 == CHUNK) {
+    // page ids of the next chunk's 16-token halves; -1: no row sees them
+    constexpr int HALVES = CHUNK / 16;
+    int page_next[HALVES];
+    auto fetch_pages = [&](int k) {
 #pragma unroll
-          for (int i = 0; i < CHUNK * PR / 32; ++i) {
-            const int u = lane + 32 * i;
-            cp_async16(dst + piece<C::rby>(u / PR, u % PR), ksrc + u * 16);
-            cp_async16(dst + C::kv_bytes + piece<C::rby>(u / PR, u % PR), vsrc + u * 16);
-          }
-        } else {
+      for (int h = 0; h < HALVES; ++h) {
+        const int t = tok0 + k * UT + 16 * h;
+        page_next[h] = wanted(k) && t < cur.hi && t + 16 > cur.lo ? __ldg(table + (t >> p.page_shift)) : -1;
+      }
+    };
+    fetch_pages(0);
+    auto issue = [&](int k) {
+      int page[HALVES];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) page[h] = page_next[h];
+      fetch_pages(k + 1);
+      if (wanted(k)) {
+        const uint32_t dst = ring + (uint32_t)(k % S) * C::stage;
+        constexpr int PR = C::rby / 16, PS = C::sby;  // 16-byte pieces of a row; of 16 rows' scales
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+          const int t = tok0 + k * UT + 16 * h;
+          const bool ok = (unsigned)page[h] < (unsigned)p.n_pages;
+          if (!ok && t < cur.hi && t + 16 > cur.lo && lane == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+          const int r0 = max(cur.lo - t, 0), r1 = ok ? min(cur.hi - t, 16) : 0;  // rows to read; the others are zeros
+          const long long row = (((long long)(ok ? page[h] : 0) * p.n_kv_heads + cur.head) << p.page_shift) +
+                                (t & (p.page_size - 1));
+          const uint8_t* ksrc = p.k + row * C::rby;
+          const uint8_t* vsrc = p.v + row * C::rby;
+          if (r0 == 0 && r1 == 16) {
+#pragma unroll
+            for (int i = 0; i < PR / 2; ++i) {
+              const int u = lane + 32 * i;
+              cp_async16(dst + piece<C::rby>(16 * h + u / PR, u % PR), ksrc + u * 16);
+              cp_async16(dst + C::kv_bytes + piece<C::rby>(16 * h + u / PR, u % PR), vsrc + u * 16);
+            }
+          } else {
 #pragma unroll 2
-          for (int i = 0; i < CHUNK * PR / 32; ++i) {
-            const int u = lane + 32 * i, r = u / PR, pc = u % PR;
-            const bool there = r >= r0 && r < r1;
-            cp_async16(dst + piece<C::rby>(r, pc), ksrc + u * 16, there);
-            cp_async16(dst + C::kv_bytes + piece<C::rby>(r, pc), vsrc + u * 16, there);
+            for (int i = 0; i < PR / 2; ++i) {
+              const int u = lane + 32 * i, r = u / PR, pc = u % PR;
+              const bool there = r >= r0 && r < r1;
+              cp_async16(dst + piece<C::rby>(16 * h + r, pc), ksrc + u * 16, there);
+              cp_async16(dst + C::kv_bytes + piece<C::rby>(16 * h + r, pc), vsrc + u * 16, there);
+            }
           }
-        }
-        if constexpr (C::q) {  // scales of all 16 rows
-          constexpr int PS = CHUNK * C::sby / 16;
-          if (lane < 2 * PS) {
-            const int i = lane % PS;
-            const uint8_t* src = (lane < PS ? p.ks : p.vs) + row * C::sby + i * 16;
-            cp_async16(dst + 2 * C::kv_bytes + (lane < PS ? 0 : CHUNK * C::sby) + i * 16, src, ok);
+          if constexpr (C::q) {
+            if (lane < 2 * PS) {
+              const int i = lane % PS;
+              const uint8_t* src = (lane < PS ? p.ks : p.vs) + row * C::sby + i * 16;
+              cp_async16(dst + 2 * C::kv_bytes + (lane < PS ? 0 : CHUNK * C::sby) + (h * PS + i) * 16, src, ok);
+            }
           }
         }
       }
@@ -388,42 +413,43 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         // of its block NaN), zero for tokens that are left out; and log2 of the largest one of
         // the values, 13 at most.
         const uint8_t* codes = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
-        constexpr int PER = 2 * CHUNK * NB / 32;  // codes of a lane: all of K or all of V
+        // Lane l takes the codes of token l % CHUNK: with 16 tokens of K or of V, with 32 of both.
+        constexpr int SETS = CHUNK / 16;
+        const int tok = lane % CHUNK;
+        const bool in = t + tok >= cur.lo && t + tok < cur.hi;
         uint32_t top = 0;
-        float f[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int tok = t + (lane * PER + i) % (CHUNK * NB) / NB;
-          const uint32_t code = codes[lane * PER + i];
-          const bool in = tok >= cur.lo && tok < cur.hi;
-          f[i] = __uint_as_float(in ? code << 23 : 0u);
-          top = max(top, in && code < 255u ? code : 0u);
-        }
-        top = __reduce_max_sync(0xffffffffu, lane >= 16 ? top : 0u);
-        ve = fminf((float)top - 127.f, 13.f);
-#pragma unroll
-        for (int i = 0; i < PER; i += 2) *reinterpret_cast<float2*>(sc_f + lane * PER + i) = make_float2(f[i], f[i + 1]);
-        __syncwarp();
-      }
-      // of this thread's tokens 2c, 2c+1, 2c+8, 2c+9
-      auto scales_of = [&](const float* base, float (*w)[NB]) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float* src = base + (2 * c + (x & 1) + 8 * (x >> 1)) * NB;
+        for (int i = 0; i < SETS; ++i) {
+          const int set = SETS == 2 ? i : lane / CHUNK;  // 0: K, 1: V
+          const uint8_t* src = codes + (set * CHUNK + tok) * NB;
+          uint32_t w[NB > 4 ? 2 : 1];
           if constexpr (NB == 2) {
-            *reinterpret_cast<float2*>(w[x]) = *reinterpret_cast<const float2*>(src);
+            w[0] = *reinterpret_cast<const uint16_t*>(src);
           } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(src);
+            if constexpr (NB > 4) w[1] = *reinterpret_cast<const uint32_t*>(src + 4);
+          }
 #pragma unroll
-            for (int y = 0; y < NB; y += 4) *reinterpret_cast<float4*>(w[x] + y) = *reinterpret_cast<const float4*>(src + y);
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t code = (w[b >> 2] >> (8 * (b & 3))) & 0xffu;
+            sc_f[(set * NB + b) * CHUNK + tok] = __uint_as_float(in ? code << 23 : 0u);
+            if (set == 1) top = max(top, in && code < 255u ? code : 0u);
           }
         }
+        top = __reduce_max_sync(0xffffffffu, top);
+        ve = fminf((float)top - 127.f, 13.f);
+        __syncwarp();
+      }
+      // of a block: this thread's tokens 2c, 2c+1 of column tile nt
+      auto scale2 = [&](int set, int blk, int nt) {
+        return *reinterpret_cast<const float2*>(sc_f + (set * NB + blk) * CHUNK + 8 * nt + 2 * c);
       };
       // ------------------------------------------------------------ scores
-      float s[MT][2][4];
+      float s[MT][TT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] = 0.f;
+        for (int i = 0; i < 4 * TT; ++i) s[mt][i >> 2][i & 3] = 0.f;
       const int mrow = (lane & 7) + ((lane >> 4) << 3), mpc = (lane >> 3) & 1;  // ldmatrix row and piece of this lane
       if constexpr (!C::q) {
 #pragma unroll
@@ -438,43 +464,46 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
       } else {
-        float kw[4][NB];
-        scales_of(sc_f, kw);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {  // a 1x32 block: two k steps
-          uint32_t f[2][2][2];                // [k step][column tile] operands
-          uint32_t b[4];
-          if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (0-7, 2blk+1), (8-15, 2blk), (8-15, 2blk+1)
-            ldm4(b, st + piece<C::rby>(mrow, 2 * blk + mpc));
+          uint32_t f[2][TT][2];               // [k step][column tile] operands
 #pragma unroll
-            for (int x = 0; x < 4; ++x) e4m3x4_f16(b[x], f[x & 1][x >> 1][0], f[x & 1][x >> 1][1]);
-          } else {                    // piece blk of tokens 0-7 and 8-15
-            const uint32_t at = st + piece<C::rby>(lane & 15, blk);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(at) : "memory");
+          for (int h = 0; h < TT / 2; ++h) {
+            uint32_t b[4];
+            if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (0-7, 2blk+1), (8-15, 2blk), (8-15, 2blk+1)
+              ldm4(b, st + piece<C::rby>(16 * h + mrow, 2 * blk + mpc));
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              uint32_t e[4];
-              e2m1x8_f16(b[nt], e);
-              f[0][nt][0] = e[0];
-              f[0][nt][1] = e[1];
-              f[1][nt][0] = e[2];
-              f[1][nt][1] = e[3];
+              for (int x = 0; x < 4; ++x) e4m3x4_f16(b[x], f[x & 1][2 * h + (x >> 1)][0], f[x & 1][2 * h + (x >> 1)][1]);
+            } else {                    // piece blk of tokens 0-7 and 8-15
+              ldm2(b, st + piece<C::rby>(16 * h + (lane & 15), blk));
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                uint32_t e[4];
+                e2m1x8_f16(b[nt], e);
+                f[0][2 * h + nt][0] = e[0];
+                f[0][2 * h + nt][1] = e[1];
+                f[1][2 * h + nt][0] = e[2];
+                f[1][2 * h + nt][1] = e[3];
+              }
             }
           }
+          uint32_t a[MT][2][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            query(mt, 2 * blk, a[mt][0]);
+            query(mt, 2 * blk + 1, a[mt][1]);
+          }
 #pragma unroll
-            for (int sp = 0; sp < 2; ++sp) {
-              uint32_t a[4];
-              query(mt, 2 * blk + sp, a);
-              mma_f16(acc[0], a, f[sp][0][0], f[sp][0][1]);
-              mma_f16(acc[1], a, f[sp][1][0], f[sp][1][1]);
+          for (int nt = 0; nt < TT; ++nt) {
+            const float2 sc = scale2(0, blk, nt);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(acc, a[mt][0], f[0][nt][0], f[0][nt][1]);
+              mma_f16(acc, a[mt][1], f[1][nt][0], f[1][nt][1]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s[mt][nt][q] = fmaf(acc[q], q & 1 ? sc.y : sc.x, s[mt][nt][q]);
             }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) s[mt][nt][q] = fmaf(acc[nt][q], kw[2 * nt + (q & 1)][blk], s[mt][nt][q]);
           }
         }
       }
@@ -485,17 +514,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[mt][i >> 2][i & 3] *= scale[mt][(i >> 1) & 1];
+        for (int i = 0; i < 4 * TT; ++i) s[mt][i >> 2][i & 3] *= scale[mt][(i >> 1) & 1];
         if (!inside) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4 * TT; ++i) {
             const int j = t + 8 * (i >> 2) + 2 * c + (i & 1), h = (i >> 1) & 1;
             if (j < lo[mt][h] || j >= hi[mt][h]) s[mt][i >> 2][i & 3] = -INFINITY;
           }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx[mt][h] = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+          mx[mt][h] = fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]);
+#pragma unroll
+          for (int nt = 1; nt < TT; ++nt) mx[mt][h] = fmaxf(mx[mt][h], fmaxf(s[mt][nt][2 * h], s[mt][nt][2 * h + 1]));
           move |= mx[mt][h] > m[mt][h] + kSlack;
         }
       }
@@ -535,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           const float mu = (m[mt][h] == -INFINITY ? 0.f : m[mt][h]) + (C::q ? ev : 0.f);
           float sum = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < TT; ++nt)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const float e = ex2(s[mt][nt][2 * h + q] - mu);
@@ -564,40 +595,42 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
       } else {
-        float vw[4][NB];
-        scales_of(sc_f + CHUNK * NB, vw);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {  // 32 columns: four column tiles with one scale for a token
-          uint32_t f[4][2];  // [column tile] operands
-          uint32_t b[4];
-          if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (8-15, 2blk), (0-7, 2blk+1), (8-15, 2blk+1)
-            ldm4t(b, vst + piece<C::rby>(vrow, 2 * blk + vpc));
 #pragma unroll
-            for (int x = 0; x < 4; ++x)  // bytes t0d0 t0d1 t1d0 t1d1 -> (t0d0, t1d0), (t0d1, t1d1)
-              e4m3x4_f16(__byte_perm(b[x], 0, 0x3120), f[2 * (x >> 1)][x & 1], f[2 * (x >> 1) + 1][x & 1]);
-          } else {                    // piece blk of tokens 0-7 and 8-15
-            const uint32_t at = vst + piece<C::rby>(vrow, blk);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(at) : "memory");
+          for (int h = 0; h < TT / 2; ++h) {
+            uint32_t f[4][2];  // [column tile] operands of 16 tokens
+            uint32_t b[4];
+            if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (8-15, 2blk), (0-7, 2blk+1), (8-15, 2blk+1)
+              ldm4t(b, vst + piece<C::rby>(16 * h + vrow, 2 * blk + vpc));
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // four codes of token 0 (low half) and of token 1 -> bytes of both tokens' code i:
-              // codes 0 and 2 in the low half of y, 1 and 3 in the low half of z
-              const uint32_t y = b[x] & 0x0F0F0F0Fu, z = (b[x] >> 4) & 0x0F0F0F0Fu;
-              uint32_t e[4];
-              e2m1x8_f16(__byte_perm(y | (y >> 12), z | (z >> 12), 0x5140), e);
+              for (int x = 0; x < 4; ++x)  // bytes t0d0 t0d1 t1d0 t1d1 -> (t0d0, t1d0), (t0d1, t1d1)
+                e4m3x4_f16(__byte_perm(b[x], 0, 0x3120), f[2 * (x >> 1)][x & 1], f[2 * (x >> 1) + 1][x & 1]);
+            } else {                    // piece blk of tokens 0-7 and 8-15
+              ldm2t(b, vst + piece<C::rby>(16 * h + vrow, blk));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f[i][x] = e[i];
+              for (int x = 0; x < 2; ++x) {
+                // four codes of token 0 (low half) and of token 1 -> bytes of both tokens' code i:
+                // codes 0 and 2 in the low half of y, 1 and 3 in the low half of z
+                const uint32_t y = b[x] & 0x0F0F0F0Fu, z = (b[x] >> 4) & 0x0F0F0F0Fu;
+                uint32_t e[4];
+                e2m1x8_f16(__byte_perm(y | (y >> 12), z | (z >> 12), 0x5140), e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i][x] = e[i];
+              }
             }
-          }
+            const float2 sc[2] = {scale2(1, blk, 2 * h), scale2(1, blk, 2 * h + 1)};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t pa[4];
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t pa[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)  // rows g, g + 8 of tokens 0-7, then of 8-15
-              pa[i] = pack_f16(s[mt][i >> 1][2 * (i & 1)] * vw[2 * (i >> 1)][blk],
-                               s[mt][i >> 1][2 * (i & 1) + 1] * vw[2 * (i >> 1) + 1][blk]);
+              for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of tokens 0-7, then of 8-15
+                const float* e = s[mt][2 * h + (i >> 1)] + 2 * (i & 1);
+                pa[i] = pack_f16(e[0] * sc[i >> 1].x, e[1] * sc[i >> 1].y);
+              }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f16(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
+              for (int i = 0; i < 4; ++i) mma_f16(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
+            }
           }
         }
       }
