@@ -162,21 +162,21 @@ struct Cfg {
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
   static constexpr int scales = q ? 2 * CHUNK * (D / 32) * 4 : 0;  // a warp's chunk of scales in FP32
-  static constexpr int ctas = D == 256 && !q ? 1 : 2;  // per SM
-  static constexpr int room = ctas == 1 ? 200 * 1024 : 100 * 1024;
+  static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;  // per SM
+  static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 66 * 1024;
   static constexpr int fit = room / (kWarps * stage);
   static constexpr int stages = fit < 8 ? fit : 8;
   static constexpr int ring = kWarps * stages * stage;
   static constexpr int opitch = D + 8;  // floats of a row where the warps join
   static constexpr int join = kWarps * RB * opitch * 4;
   static constexpr int qfrag = MT * (D / 16) * 512;
-  static constexpr int head = 2048;     // maxima and sums where the warps join, and the rows' query scales
+  static constexpr int head = 1024 * MT;  // maxima and sums where the warps join, and the rows' query scales
   static constexpr int weights = 160 * ctas * RB * 8;  // and sums of an item's parts where CTAs join (up to 160 SMs)
   static constexpr int max0 = ring > join ? ring : join, max1 = max0 > weights ? max0 : weights;
   static constexpr int body = max1 > (int)sizeof(PlanSmem) ? max1 : (int)sizeof(PlanSmem);
   static constexpr int smem = qfrag + head + body + kWarps * scales;
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
-  static constexpr bool q_regs = D <= 128 && MT == 1;  // the queries' operands stay in registers
+  static constexpr bool q_regs = D <= 128 && MT == 1 && !q;  // the queries' operands stay in registers
 };
 
 // Column of the values that accumulator half h (columns 2c and 2c+1 of tile nt) stands for.
