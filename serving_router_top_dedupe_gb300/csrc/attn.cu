@@ -32,7 +32,18 @@ int sm_count() {
 
 // Counters, a stand-in for the caller's error word, and two partial results for each CTA: of
 // head_dim + 2 floats for 16 rows (few rows: two CTAs per SM), or 256 or 128 rows (chunks: one).
-size_t workspace_need(int n_sm, int D) { return kCounterBytes + 256 + (size_t)n_sm * 2 * (D == 256 ? 128 : 256) * (D + 2) * 4; }
+size_t partial_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * (D == 256 ? 128 : 256) * (D + 2) * 4; }
+
+// What a call cannot do without; then, for the decoded copy of a quantised cache's pages: where
+// each sequence's pages begin in it, whether it had room, and the copy.
+size_t workspace_least(int n_sm, int D) { return kCounterBytes + 256 + partial_bytes(n_sm, D); }
+constexpr size_t kStageHead = kMaxSeqs * 4 + 256;
+constexpr size_t kStageBytes = (size_t)512 << 20;
+
+// The decoded copy costs reading the codes and writing 4 bytes per pair of elements once; without
+// it every block of rows decodes what it reads.  For 2048 rows of a head over 16384 tokens
+// ... the two meet near four blocks.
+constexpr int kStageRows = 1024;
 
 ft_status check_heads(const char* name, int n_heads, int n_kv_heads, int head_dim) {
   if (n_kv_heads < 1 || n_kv_heads > 1024 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128)
@@ -53,7 +64,7 @@ extern "C" ft_status ft_attn_workspace(int n_heads, int n_kv_heads, int head_dim
   if (ft_status st = kv::check_heads("ft_attn_workspace", n_heads, n_kv_heads, head_dim)) return st;
   const int n_sm = kv::sm_count();
   if (!n_sm) return kv_fail(FT_ERR_CUDA, "ft_attn_workspace: no device");
-  *bytes_out = kv::workspace_need(n_sm, head_dim);
+  *bytes_out = kv::workspace_least(n_sm, head_dim) + kv::kStageHead + kv::kStageBytes;
   return FT_OK;
 }
 
@@ -86,9 +97,9 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
                    a->q_stride, a->out_stride);
   const int n_sm = kv::sm_count();
   if (!n_sm) return kv_fail(FT_ERR_CUDA, "%s: no device", name);
-  if (a->workspace_bytes < kv::workspace_need(n_sm, c->head_dim))
-    return kv_fail(FT_ERR_CAPACITY, "%s: the workspace has %zu bytes, %zu are needed", name, a->workspace_bytes,
-                   kv::workspace_need(n_sm, c->head_dim));
+  const size_t least = kv::workspace_least(n_sm, c->head_dim);
+  if (a->workspace_bytes < least)
+    return kv_fail(FT_ERR_CAPACITY, "%s: the workspace has %zu bytes, %zu are needed", name, a->workspace_bytes, least);
 
   kv::AttnParams p{};
   p.k = static_cast<const uint8_t*>(c->k);
@@ -123,7 +134,41 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, int, cudaStream_t);
   static const Kernel kernels[2][3] = {{kv::attn_rows_bf16, kv::attn_rows_mxfp8, kv::attn_rows_mxfp4},
                                        {kv::attn_chunk_bf16, kv::attn_chunk_mxfp8, kv::attn_chunk_mxfp4}};
-  const int rows = (int)((long long)a->max_new * p.group < 33 ? a->max_new * p.group : 33);  // of one cache head
-  const cudaError_t e = kernels[rows > 32][c->kv_type](p, c->head_dim, rows, n_sm, s);
+  const long long rows = (long long)a->max_new * p.group;  // of one cache head of a sequence, at most
+  cudaError_t e = cudaSuccess;
+  if (c->kv_type != FT_KV_BF16 && rows >= kv::kStageRows && a->workspace_bytes >= least + kv::kStageHead + kv::kStageBytes) {
+    // many rows over a quantised cache: its pages are decoded once
+    uint8_t* at = static_cast<uint8_t*>(a->workspace) + least;
+    const size_t page = (size_t)c->n_kv_heads * c->page_size * c->head_dim * 2;
+    kv::StageParams st{};
+    st.a = p;
+    st.cap_pages = (int)(kv::kStageBytes / 2 / page < (1u << 24) ? kv::kStageBytes / 2 / page : 1u << 24);
+    st.base = reinterpret_cast<int32_t*>(at);
+    st.have = st.base + kv::kMaxSeqs;
+    st.k = reinterpret_cast<uint16_t*>(at + kv::kStageHead);
+    st.v = st.k + (size_t)st.cap_pages * page / 2;
+    e = kv::stage_pages(st, c->kv_type, c->head_dim, n_sm, s);
+    // how many pages the batch has is known on the device; where the tables could hold more than
+    // there is room for, both kernels are launched and one of them has nothing to do
+    const bool fits = (long long)a->n_seqs * a->table_stride <= st.cap_pages;
+    if (e == cudaSuccess && !fits) {
+      kv::AttnParams direct = p;
+      direct.have = st.have;
+      direct.want = 0;
+      e = kernels[1][c->kv_type](direct, c->head_dim, 33, n_sm, s);
+    }
+    if (e == cudaSuccess) {
+      p.k = reinterpret_cast<const uint8_t*>(st.k);
+      p.v = reinterpret_cast<const uint8_t*>(st.v);
+      p.ks = p.vs = nullptr;
+      p.n_pages = st.cap_pages;
+      p.staged = st.base;
+      p.have = fits ? nullptr : st.have;
+      p.want = 1;
+      e = kernels[1][FT_KV_BF16](p, c->head_dim, 33, n_sm, s);
+    }
+  } else {
+    e = kernels[rows > 32][c->kv_type](p, c->head_dim, (int)(rows < 33 ? rows : 33), n_sm, s);
+  }
   return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }

@@ -53,15 +53,16 @@ struct Cfg {
   static constexpr int threads = 32 * (soft_warps + (q ? 12 : 4));
   static constexpr int qbytes = tiles * stage;
   static constexpr int out_bytes = soft_warps * 32 * 128;  // 64 output columns of each warp's rows
-  static constexpr int smem = 1024 + qbytes + 2 * stages * stage + out_bytes + 512;
+  static constexpr int walks = q ? 8 * 96 : 0;             // where the loaders' walks wait
+  static constexpr int smem = 1024 + qbytes + 2 * stages * stage + out_bytes + 512 + walks;
   // Registers of the softmax, MMA and loader warps out of those that the block starts with:
   // BF16, two tiles (168 x 384 = 64512): 208 x 256 + 88 x 128 = 64512;
   // quantised, two tiles (96 x 640 = 61440): 136 x 256 + 80 x 128 + 64 x 256 = 61440;
-  // quantised, one tile (128 x 512 = 65536): 192 x 128 + 96 x 128 + 112 x 256 = 65536.
+  // quantised, one tile (128 x 512 = 65536): 192 x 128 + 64 x 128 + 128 x 256 = 65536.
   static constexpr bool split = q || tiles == 2;
   static constexpr int soft_regs = !q ? 208 : tiles == 2 ? 136 : 192;
-  static constexpr int mma_regs = !q ? 88 : tiles == 2 ? 80 : 96;
-  static constexpr int load_regs = tiles == 2 ? 64 : 112;
+  static constexpr int mma_regs = !q ? 88 : tiles == 2 ? 80 : 64;
+  static constexpr int load_regs = tiles == 2 ? 64 : 128;
   static constexpr int batch = !q && tiles == 2 ? 128 : 64;  // score columns that a softmax thread holds
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
   static constexpr int o_col = 256;  // TMEM: S (and P) at 0 and 128, O behind
@@ -197,12 +198,19 @@ __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
     out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
+// What a loader keeps of an item while it is at it (the rest of its walk waits in shared memory).
+struct Part {
+  const int32_t* table;  // the sequence's row of the page table
+  int len, lo, head;
+  int t, left;           // first token of the next tile, tiles left in this CTA's part of the item
+};
+
 // Page ids of a tile: lane i (and i + 8, ...) holds that of tokens [t + 16 i, t + 16 i + 16), or
 // -1 where no row sees them.
-__device__ __forceinline__ int tile_pages(const AttnParams& p, const Cursor& cur, int t, int lane) {
+__device__ __forceinline__ int tile_pages(const AttnParams& p, const Part& it, int t, int lane) {
   const int tok = t + 16 * (lane & 7);
-  if (tok >= cur.len || tok + 16 <= cur.lo) return -1;
-  const int page = __ldg(p.page_table + (long long)cur.seq * p.table_stride + (tok >> p.page_shift));
+  if (tok >= it.len || tok + 16 <= it.lo) return -1;
+  const int page = __ldg(it.table + (tok >> p.page_shift));
   if ((unsigned)page < (unsigned)p.n_pages) return page;
   atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
   return -1;
@@ -220,12 +228,12 @@ struct Raw {
 };
 
 template <int TYPE, int D>
-__device__ __forceinline__ void raw_load(const AttnParams& p, const Cursor& cur, int t, int pages, const uint8_t* base,
+__device__ __forceinline__ void raw_load(const AttnParams& p, const Part& it, int t, int pages, const uint8_t* base,
                                          const uint8_t* scales, int lt, Raw<TYPE, D>& x) {
   constexpr int PR = Raw<TYPE, D>::PR;
   const int lane = lt & 31, in_page = p.page_size - 1;
   auto row_at = [&](int r, int page) {  // row of the cache; a page that is not there: some row
-    return ((max(page, 0) * p.n_kv_heads + cur.head) << p.page_shift) + ((t + r) & in_page);
+    return ((max(page, 0) * p.n_kv_heads + it.head) << p.page_shift) + ((t + r) & in_page);
   };
 #pragma unroll
   for (int i = 0; i < PR; ++i) {
@@ -236,7 +244,7 @@ __device__ __forceinline__ void raw_load(const AttnParams& p, const Cursor& cur,
   constexpr int per = 32 / PR;  // rows of a warp's piece i
   const int r = ((lt & ~31) + 128 * (lane / per)) / PR + lane % per;
   const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
-  const bool seen = page >= 0 && t + r < cur.len && t + r >= cur.lo;
+  const bool seen = page >= 0 && t + r < it.len && t + r >= it.lo;
   const uint8_t* src = scales + (size_t)(uint32_t)row_at(r, page) * (D / 32);
   if constexpr (D == 64) {
     const uint32_t s = __ldg(reinterpret_cast<const uint16_t*>(src));
@@ -294,6 +302,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   uint64_t* done = q_full + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* walks = reinterpret_cast<uint8_t*>(bars) + 512;
+  static_assert(sizeof(ChunkWalk<TYPE, D>) <= 96, "a walk's place");
   auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -315,6 +325,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   }
   pdl_wait();
   pdl_trigger();
+  if (p.have && __ldg(p.have) != p.want) return;
   ChunkWalk<TYPE, D> wk;
   long long per;
   if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kLeast, wk, per)) return;
@@ -341,7 +352,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_tm = tl + C::o_col + rt * D;
-    const float c = fabsf(p.scale_log2) * left_in(TYPE);
+    // never zero: what is masked is -inf before it is scaled
+    const float c = fmaxf(fabsf(p.scale_log2) * left_in(TYPE), 1e-30f);
     const uint64_t c2 = f2(c, c);
 
     // an item's queries into shared memory, once no product reads the last ones
@@ -728,7 +740,10 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         const int t = wk.tile() * KT, tok = t + (pg << shift);
         // a page whose tokens are there and may be seen by some row
         const bool there = tok < cur.len && tok + ps > cur.lo;
-        int page = there ? __ldg(p.page_table + (long long)cur.seq * p.table_stride + (tok >> shift)) : 0;
+        int page = 0;
+        if (there)
+          page = p.staged ? __ldg(p.staged + cur.seq) + (tok >> shift)
+                          : __ldg(p.page_table + (long long)cur.seq * p.table_stride + (tok >> shift));
         const bool good = there && (unsigned)page < (unsigned)p.n_pages;
         const uint32_t pages = __ballot_sync(0xffffffffu, good) & ((1u << npg) - 1u);
         const bool bad = __any_sync(0xffffffffu, there && !good);
@@ -782,18 +797,41 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     const uint8_t* scales = kv ? p.vs : p.ks;
     uint8_t* my_ring = ring + kv * NS * C::stage;
     uint32_t st = 0, ph = 0;
+    ChunkWalk<TYPE, D>* my_walk = reinterpret_cast<ChunkWalk<TYPE, D>*>(walks) + (warp - C::load_warp);
+    Part it;
+    auto enter = [&](const ChunkWalk<TYPE, D>& w) {
+      it.table = p.page_table + (long long)w.cur.seq * p.table_stride;
+      it.len = w.cur.len;
+      it.lo = w.cur.lo;
+      it.head = w.cur.head;
+      it.t = w.tile() * KT;
+      it.left = w.more() ? (int)(w.end() - w.w) : 0;
+      __syncwarp();
+      if (lane == 0) *my_walk = w;
+      __syncwarp();
+    };
+    // to the next tile; it.left is 0 behind the last one
+    auto next = [&]() {
+      it.t += KT;
+      if (--it.left == 0) {
+        ChunkWalk<TYPE, D> w = *my_walk;
+        w.next_item(p);
+        enter(w);
+      }
+    };
+    enter(wk);
     Raw<TYPE, D> x;
-    raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, tile_pages(p, wk.cur, wk.tile() * KT, lane), base, scales, lt, x);
-    wk.next(p);
-    int pages = wk.more() ? tile_pages(p, wk.cur, wk.tile() * KT, lane) : -1;
+    raw_load<TYPE, D>(p, it, it.t, tile_pages(p, it, it.t, lane), base, scales, lt, x);
+    next();
+    int pages = it.left ? tile_pages(p, it, it.t, lane) : -1;
     for (bool last = false; !last;) {
       if (!wait_all(empty + kv * NS + st, ph ^ 1u)) break;
       raw_store<TYPE, D>(my_ring + st * C::stage, lt, x);
-      last = !wk.more();
+      last = it.left == 0;
       if (!last) {
-        raw_load<TYPE, D>(p, wk.cur, wk.tile() * KT, pages, base, scales, lt, x);
-        wk.next(p);
-        if (wk.more()) pages = tile_pages(p, wk.cur, wk.tile() * KT, lane);
+        raw_load<TYPE, D>(p, it, it.t, pages, base, scales, lt, x);
+        next();
+        if (it.left) pages = tile_pages(p, it, it.t, lane);
       }
       fence_async();
       __syncwarp();

@@ -69,6 +69,13 @@ struct AttnParams {
   uint32_t* counters;  // [kMaxCtas], zero between calls
   float* partials;
   uint32_t* error_word;  // never NULL
+  // A copy of the pages that the batch sees, decoded to BF16 (stage_pages): k, v and n_pages are
+  // the copy's, and page j of sequence s is its page staged[s] + j.  NULL: the cache itself.
+  const int32_t* staged;
+  // Whether the copy had room is known on the device only: a kernel whose `want` differs from
+  // *have returns at once.  NULL: no such choice.
+  const int32_t* have;
+  int want;
 };
 
 constexpr int kMaxCtas = 4096;                     // CTAs of one attention launch, at most
@@ -181,6 +188,16 @@ struct Walk {
     return true;
   }
 };
+
+// The decoded copy of a batch's pages.
+struct StageParams {
+  AttnParams a;        // over the quantised cache
+  uint16_t *k, *v;     // [cap_pages][n_kv_heads][page_size][D] BF16
+  int cap_pages;
+  int32_t* base;       // [kMaxSeqs] staged[] of AttnParams
+  int32_t* have;       // 1: the copy holds every page, 0: no room
+};
+cudaError_t stage_pages(const StageParams& p, int type, int D, int n_sm, cudaStream_t s);
 
 struct PlanSmem {
   long long sum[kMaxSeqs];  // counts of a sequence's blocks (one head), then their prefix sums

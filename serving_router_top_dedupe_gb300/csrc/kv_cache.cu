@@ -204,6 +204,109 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
   }
 }
 
+// Decodes every page that a batch's new tokens may see, once, into a BF16 copy.  One warp takes
+// one page of one head, of K (blockIdx.y 0) or V; lanes take 1x32 blocks, so that a warp reads
+// and writes whole lines.  Reading the codes and writing twice or four times their bytes bounds
+// it.
+constexpr int kStageThreads = 256;
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageParams p) {
+  constexpr int NB = D / 32, NW = kStageThreads / 32, PER = kMaxSeqs / kStageThreads;
+  __shared__ int before[kMaxSeqs + 1];  // pages of the sequences before
+  __shared__ int part[NW];
+  pdl_wait();
+  pdl_trigger();
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int first[PER], count[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = tid * PER + i;
+    first[i] = count[i] = 0;
+    if (s < a.n_seqs) {
+      int q0, n, len;
+      bool bad;
+      seq_range(a, s, q0, n, len, bad);
+      if (n > 0 && len > 0) {
+        const int lo = a.window > 0 ? max(len - n - a.window + 1, 0) : 0;
+        first[i] = lo >> a.page_shift;
+        count[i] = ((len + a.page_size - 1) >> a.page_shift) - first[i];
+      }
+    }
+    sum += count[i];  // a sequence has at most 2^26 pages; a sum beyond 2^31 is caught below
+    if (sum < 0) sum = 1 << 30;
+  }
+  int x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = min((long long)x + y, (long long)(1 << 30));
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long run = x - sum;
+  long long total = 0;
+  for (int i = 0; i < NW; ++i) {
+    if (i < warp) run += part[i];
+    total += part[i];
+  }
+  const bool room = total <= p.cap_pages;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.have = room;
+  if (!room) return;
+  int at = (int)run;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = tid * PER + i;
+    if (s < a.n_seqs) {
+      before[s] = at;
+      if (blockIdx.x == 0 && blockIdx.y == 0) p.base[s] = at - first[i];
+      at += count[i];
+    }
+  }
+  __syncthreads();
+  const bool is_v = blockIdx.y != 0;
+  const uint8_t* codes0 = is_v ? a.v : a.k;
+  const uint8_t* scales0 = is_v ? a.vs : a.ks;
+  uint16_t* out0 = is_v ? p.v : p.k;
+  const long long items = total * a.n_kv_heads;
+  for (long long it = (long long)blockIdx.x * NW + warp; it < items; it += (long long)gridDim.x * NW) {
+    const int sp = (int)(it / a.n_kv_heads), head = (int)(it - (long long)sp * a.n_kv_heads);
+    int s = 0;  // the last sequence that begins at or before this page and has any
+    for (int lo = 0, hi = a.n_seqs; lo < hi;) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= sp) {
+        s = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid;
+      }
+    }
+    int q0, n, len;
+    bool bad;
+    seq_range(a, s, q0, n, len, bad);
+    const int lo = a.window > 0 ? max(len - n - a.window + 1, 0) : 0;
+    const int j = sp - before[s] + (lo >> a.page_shift);  // page of the sequence
+    const int page = __ldg(a.page_table + (long long)s * a.table_stride + j);
+    const bool ok = (unsigned)page < (unsigned)a.n_pages;
+    if (!ok && lane == 0) atomicOr(a.error_word, FT_DEVERR_BAD_INDEX);
+    const long long from = ((long long)(ok ? page : 0) * a.n_kv_heads + head) << a.page_shift;
+    const long long to = ((long long)sp * a.n_kv_heads + head) << a.page_shift;
+    for (int b = lane; b < a.page_size * NB; b += 32) {
+      uint4 c[2], y[4];
+      const uint4* codes = reinterpret_cast<const uint4*>(codes0 + from * row_bytes(TYPE, D) + b * row_bytes(TYPE, 32));
+      c[0] = __ldg(codes);
+      if (TYPE == FT_KV_MXFP8) c[1] = __ldg(codes + 1);
+      const uint32_t scale = ok ? __ldg(scales0 + from * NB + b) : 0u;
+      stands_for<TYPE>(c, scale, y);
+      if (!ok) y[0] = y[1] = y[2] = y[3] = make_uint4(0, 0, 0, 0);
+      uint4* dst = reinterpret_cast<uint4*>(out0 + to * D + b * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = y[i];
+    }
+  }
+}
+
 template <int TYPE, int D>
 cudaError_t launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
   const long long threads = (long long)p.n_tokens * p.n_kv_heads * (D / 32);
@@ -216,6 +319,14 @@ template <int TYPE>
 cudaError_t launch_rows_d(int D, const RowsParams& p, bool write, cudaStream_t s) {
   return D == 64 ? launch_rows_t<TYPE, 64>(p, write, s) : D == 128 ? launch_rows_t<TYPE, 128>(p, write, s)
                                                                    : launch_rows_t<TYPE, 256>(p, write, s);
+}
+
+template <int TYPE>
+cudaError_t launch_stage(const StageParams& p, int D, int n_sm, cudaStream_t s) {
+  const dim3 grid(n_sm * 4, 2);
+  return D == 64 ? launch_k(stage_kernel<TYPE, 64>, grid, dim3(kStageThreads), 0, s, true, p)
+         : D == 128 ? launch_k(stage_kernel<TYPE, 128>, grid, dim3(kStageThreads), 0, s, true, p)
+                    : launch_k(stage_kernel<TYPE, 256>, grid, dim3(kStageThreads), 0, s, true, p);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -258,6 +369,11 @@ ft_status rows_call(const char* name, const ft_kv_cache* c, int n_tokens, const 
 }
 
 }  // namespace
+
+cudaError_t stage_pages(const StageParams& p, int type, int D, int n_sm, cudaStream_t s) {
+  return type == FT_KV_MXFP8 ? launch_stage<FT_KV_MXFP8>(p, D, n_sm, s) : launch_stage<FT_KV_MXFP4>(p, D, n_sm, s);
+}
+
 }  // namespace kv
 }  // namespace ft
 
