@@ -586,7 +586,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
           if (lane == 0) *counter = 0u;
           auto part = [&](int x) { return p.partials + (size_t)(2 * x + (x == ca ? 1 : 0)) * C::slot_floats; };
           float mm = -INFINITY, ll = 0.f;
+#pragma unroll 8
           for (int x = ca; x <= cb; ++x) mm = fmaxf(mm, __ldcg(part(x) + C::RB * D + at));
+#pragma unroll 8
           for (int x = ca; x <= cb; ++x)
             ll += __ldcg(part(x) + C::RB * (D + 1) + at) *
                   (mm == -INFINITY ? 0.f : ex2(__ldcg(part(x) + C::RB * D + at) - mm));
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
               float acc[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
               for (int x = ca; x <= cb; ++x) {
                 const float wx = mm == -INFINITY ? 0.f : ex2(__ldcg(part(x) + C::RB * D + at) - mm);
 #pragma unroll
@@ -888,7 +890,7 @@ cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
     if (e == cudaSuccess) e = page_map(&tv, p.v, D, p);
   }
   static std::atomic<uint64_t> ready{0};  // devices whose limit is set
-  if (e == cudaSuccess) e = raise_smem(attn_chunk_kernel<TYPE, D>, C::smem, ready);
+  if (e == cudaSuccess) e = prepare_kernel(attn_chunk_kernel<TYPE, D>, C::smem, ready);
   if (e != cudaSuccess) return e;
   return launch_k(attn_chunk_kernel<TYPE, D>, dim3(n_sm), dim3(C::threads), C::smem, s, true, tk, tv, p);
 }

@@ -742,28 +742,35 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           put_lse(r, mm, ll);
         }
         __syncthreads();
-        // two 16-byte pieces of a thread at a time, the parts in their order, many loads in flight
+        // four 16-byte pieces of a thread at a time, the parts in their order: many loads in flight
         const int pieces = rows * (D / 4);
-        for (int i0 = tid; i0 < pieces; i0 += 2 * kThreads) {
-          const int i1 = i0 + kThreads < pieces ? i0 + kThreads : i0;
-          const int row0 = i0 / (D / 4), row1 = i1 / (D / 4);
-          float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-#pragma unroll 8
+        for (int i0 = tid; i0 < pieces; i0 += 4 * kThreads) {
+          float4 v[4];
+          int row[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            row[e] = min(i0 + e * kThreads, pieces - 1) / (D / 4);
+          }
+#pragma unroll 4
           for (int x = 0; x < np; ++x) {
             const float4* src = reinterpret_cast<const float4*>(part(first + x));
-            const float4 u0 = __ldcg(src + i0), u1 = __ldcg(src + i1);
-            const float f0 = weight[x * RB + row0], f1 = weight[x * RB + row1];
-            v0.x += u0.x * f0;
-            v0.y += u0.y * f0;
-            v0.z += u0.z * f0;
-            v0.w += u0.w * f0;
-            v1.x += u1.x * f1;
-            v1.y += u1.y * f1;
-            v1.z += u1.z * f1;
-            v1.w += u1.w * f1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (i0 + e * kThreads < pieces) {
+                const float4 u = __ldcg(src + i0 + e * kThreads);
+                const float f = weight[x * RB + row[e]];
+                v[e].x += u.x * f;
+                v[e].y += u.y * f;
+                v[e].z += u.z * f;
+                v[e].w += u.w * f;
+              }
+            }
           }
-          put(row0, i0 % (D / 4), v0, row_l[row0] == 0.f ? 0.f : 1.f / row_l[row0]);
-          if (i1 != i0) put(row1, i1 % (D / 4), v1, row_l[row1] == 0.f ? 0.f : 1.f / row_l[row1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i0 + e * kThreads < pieces)
+              put(row[e], (i0 + e * kThreads) % (D / 4), v[e], row_l[row[e]] == 0.f ? 0.f : 1.f / row_l[row[e]]);
         }
       }
     }
@@ -777,7 +784,7 @@ template <int TYPE, int D, int MT>
 cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
   using C = Cfg<TYPE, D, MT>;
   static std::atomic<uint64_t> ready{0};  // devices whose limit is set
-  cudaError_t e = raise_smem(attn_rows_kernel<TYPE, D, MT>, C::smem, ready);
+  cudaError_t e = prepare_kernel(attn_rows_kernel<TYPE, D, MT>, C::smem, ready);
   if (e != cudaSuccess) return e;
   const int grid = n_sm * C::ctas;
   // an item's parts are at most all CTAs: their weights must fit where the CTAs join

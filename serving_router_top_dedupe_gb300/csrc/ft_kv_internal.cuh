@@ -30,15 +30,18 @@ __host__ __device__ constexpr float left_in(int type) { return type == FT_KV_MXF
 
 inline int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
 
-// Sets a kernel's shared-memory limit on the current device, once.
+// Sets a kernel's shared-memory limit on the current device, once.  All of these kernels ask
+// for the same split of an SM's memory, the largest for shared memory: launches overlap, and an
+// SM that a small kernel had switched to another split would take fewer CTAs of the next.
 template <typename K>
-cudaError_t raise_smem(K kernel, int bytes, std::atomic<uint64_t>& ready) {
+cudaError_t prepare_kernel(K kernel, int bytes, std::atomic<uint64_t>& ready) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bytes > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) ready.fetch_or(bit);
   return e;
 }

@@ -311,8 +311,10 @@ template <int TYPE, int D>
 cudaError_t launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
   const long long threads = (long long)p.n_tokens * p.n_kv_heads * (D / 32);
   const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
-  return write ? launch_k(rows_kernel<TYPE, D, true>, grid, dim3(kThreads), 0, s, true, p)
-               : launch_k(rows_kernel<TYPE, D, false>, grid, dim3(kThreads), 0, s, true, p);
+  static std::atomic<uint64_t> ready[2];
+  const auto kernel = write ? rows_kernel<TYPE, D, true> : rows_kernel<TYPE, D, false>;
+  const cudaError_t e = prepare_kernel(kernel, 0, ready[write]);
+  return e == cudaSuccess ? launch_k(kernel, grid, dim3(kThreads), 0, s, true, p) : e;
 }
 
 template <int TYPE>
@@ -321,12 +323,17 @@ cudaError_t launch_rows_d(int D, const RowsParams& p, bool write, cudaStream_t s
                                                                    : launch_rows_t<TYPE, 256>(p, write, s);
 }
 
+template <int TYPE, int D>
+cudaError_t launch_stage_t(const StageParams& p, int n_sm, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = prepare_kernel(stage_kernel<TYPE, D>, 0, ready);
+  return e == cudaSuccess ? launch_k(stage_kernel<TYPE, D>, dim3(n_sm * 4, 2), dim3(kStageThreads), 0, s, true, p) : e;
+}
+
 template <int TYPE>
 cudaError_t launch_stage(const StageParams& p, int D, int n_sm, cudaStream_t s) {
-  const dim3 grid(n_sm * 4, 2);
-  return D == 64 ? launch_k(stage_kernel<TYPE, 64>, grid, dim3(kStageThreads), 0, s, true, p)
-         : D == 128 ? launch_k(stage_kernel<TYPE, 128>, grid, dim3(kStageThreads), 0, s, true, p)
-                    : launch_k(stage_kernel<TYPE, 256>, grid, dim3(kStageThreads), 0, s, true, p);
+  return D == 64 ? launch_stage_t<TYPE, 64>(p, n_sm, s) : D == 128 ? launch_stage_t<TYPE, 128>(p, n_sm, s)
+                                                                   : launch_stage_t<TYPE, 256>(p, n_sm, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
