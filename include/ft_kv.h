@@ -30,7 +30,8 @@ extern "C" {
  * x * 2^-e rounded to nearest, ties to even, limited to +-m (magnitudes beyond 57344 or
  * 49152 saturate).  A block that holds a NaN or an infinity gets scale code 255 and reads
  * back as NaN.  What an element stands for (element * 2^e) is always a BF16 number, so
- * reading back and attention work on exactly the stored values. */
+ * reading back and attention work on exactly the stored values.  Pages filled by other means
+ * than ft_kv_write keep to these scales, and hold no NaN element codes (E4M3 0x7f, 0xff). */
 typedef enum { FT_KV_BF16 = 0, FT_KV_MXFP8 = 1, FT_KV_MXFP4 = 2 } ft_kv_type;
 
 /* Device error bit of the calls below: a slot, page id, offset or length in a device array

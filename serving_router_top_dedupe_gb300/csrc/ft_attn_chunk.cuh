@@ -27,16 +27,12 @@ namespace ft {
 namespace kv {
 namespace chunk {
 
-using rows::e2m1_bits;
-using rows::e4m3_bits;
 using rows::ex2;
-using rows::mul2;
-using rows::multiplier;
 using rows::pack;
 
 constexpr int KT = 128;           // cached tokens of a tile
 constexpr int PANEL = KT * 128;   // bytes of 64 columns of a tile: rows of 128 bytes, 128-byte swizzle
-constexpr int kLeast = 4;         // counts of a CTA's share, at least
+constexpr float kJoin = 1.2f;     // tiles' time that a part of an item costs the join
 constexpr int OV = 2;             // counts of an item besides its tiles
 constexpr float kSlack = 8.f;     // log2 units by which scores may pass the running maximum
 
@@ -170,10 +166,33 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int 
 template <int TYPE, int D>
 using ChunkWalk = Walk<Cfg<TYPE, D>::RB, KT, OV>;
 
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Two E4M3 codes in the high bytes of both halves -> the BF16 numbers they stand for, times 2^-120.
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) { return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u); }
+// Nibble I of both halves -> the BF16 numbers their E2M1 codes stand for, times 2^-126.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_bits(uint32_t w) {
+  const uint32_t mag = I == 0 ? w << 6 : I == 1 ? w << 2 : I == 2 ? w >> 2 : w >> 6;
+  const uint32_t sgn = w << (12 - 4 * I);
+  return (mag & 0x01C001C0u) | (sgn & 0x80008000u);
+}
+
+// Scale code -> a pair of BF16 multipliers: 2^e (NaN for code 255) times what the codes' bits lack.
+template <int TYPE>
+__device__ __forceinline__ uint32_t multiplier(uint32_t code) {
+  constexpr uint32_t lack = TYPE == FT_KV_MXFP8 ? 0x7B807B80u   // 2^120
+                                                : 0x76807680u;  // 2^110: 2^-16 is left in
+  return mul2((code << 7 | (code + 1) >> 8) * 0x00010001u, lack);
+}
+
 // 16 bytes of codes -> 16 (MXFP8) or 32 (MXFP4) BF16 values in their order.
 template <int TYPE>
 __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
-  const uint32_t m = multiplier<TYPE>(scale * 0x01000100u);
+  const uint32_t m = multiplier<TYPE>(scale);
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[16];
   if (TYPE == FT_KV_MXFP8) {
@@ -328,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   if (p.have && __ldg(p.have) != p.want) return;
   ChunkWalk<TYPE, D> wk;
   long long per;
-  if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kLeast, wk, per)) return;
+  if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kJoin, wk, per)) return;
   if (warp == C::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(tmem_slot))
                  : "memory");
@@ -430,6 +449,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       bool first = true;  // no product with V yet
       const int steps = (int)(wk.end() - wk.w);
       int t = wk.tile() * KT;
+      const int t_first = t;
       for (int j = 0; j < steps && rows > 0; ++j, ++step, t += KT) {
         const int u = T == 2 ? rt : (int)(step & 1);
         const uint32_t s_tm = tl + 128 * u;
@@ -437,38 +457,35 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         s_ph ^= 1u << u;
         tc_after();
         const bool edge = t < lo_max || t + KT > hi_min;
-        // scores that this row does not see become -inf
+        // scores that this row does not see become -inf; a bit for each of 32 columns
         auto mask = [&](uint32_t* s, int col, int n) {
 #pragma unroll
-          for (int c16 = 0; c16 < n; c16 += 16) {
-            const int a = t + col + c16;
-            if (a >= lo_max && a + 16 <= hi_min) continue;  // every row of the tile sees these
+          for (int c32 = 0; c32 < n; c32 += 32) {
+            const int a = t + col + c32;
+            if (a >= lo_max && a + 32 <= hi_min) continue;  // every row of the tile sees these
+            const int l0 = min(max(lo - a, 0), 32), h0 = min(max(hi - a, 0), 32);
+            const uint32_t seen = (uint32_t)((1ull << h0) - 1ull) & (uint32_t)(~0ull << l0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if ((uint32_t)(a + i - lo) >= (uint32_t)(hi - lo)) s[c16 + i] = 0xff800000u;
+            for (int i = 0; i < 32; ++i)
+              if (!(seen & (1u << i))) s[c32 + i] = 0xff800000u;
           }
         };
         constexpr int BC = C::batch;  // columns read from TMEM at once
         uint32_t pr[64];
         float mx = -INFINITY;
         uint64_t sum0, sum1;
-        if (first) {  // the first maximum
+        if (first) {  // a guess at the first maximum: that of 32 columns
+          uint32_t s[32];
+          tld<32>(s_tm, s);
+          tld_wait<32>(s);
+          if (edge) mask(s, 0, 32);
 #pragma unroll
-          for (int b = 0; b < KT / BC; ++b) {
-            uint32_t s[BC];
-#pragma unroll
-            for (int i = 0; i < BC; i += 32) tld<32>(s_tm + b * BC + i, s + i);
-            tld_wait<BC>(s);
-            if (edge) mask(s, b * BC, BC);
-#pragma unroll
-            for (int i = 0; i < BC; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
-          }
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
           m = mx * c;
-          if (!(m > -INFINITY)) m = -INFINITY;  // nothing seen, or only NaN
         }
         for (;;) {
-          // probabilities against the running maximum as it is; a score that passes it by too
-          // much is found on the way and starts the tile again
+          // Probabilities against the running maximum as it is; a score that passes it by too
+          // much is found on the way and starts the tile again.
           const float mu = m == -INFINITY ? 0.f : m;
           const uint64_t nm = f2(-mu, -mu);
           sum0 = sum1 = 0;
@@ -537,6 +554,26 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       tc_after();
       int ca, cb;
       piece_owners(cur, per, ca, cb);
+      // Sums that are not finite, because of values that the row does not see?  `use` takes what
+      // is right for them: columns of a lane, row.
+      float bad = 0.f;
+      auto look = [&](const uint32_t* o) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) bad = fmaf(__uint_as_float(o[i]), 0.f, bad);
+      };
+      auto redo = [&](auto use) {
+        const int a = max(t_first, cur.lo), b = min(t, cur.len);  // the part's tokens
+        uint32_t rows_bad = __ballot_sync(0xffffffffu, bad != bad && r < rows && (lo > a || hi < b));
+        while (rows_bad) {
+          const int x = __ffs(rows_bad) - 1;
+          rows_bad &= rows_bad - 1;
+          float again[D / 32];
+          const int see_lo = __shfl_sync(0xffffffffu, lo, x), see_hi = __shfl_sync(0xffffffffu, hi, x);
+          if (redo_row<TYPE, D>(p, cur, rbase + (warp & 3) * 32 + x, see_lo, see_hi, a, b, __shfl_sync(0xffffffffu, m, x), lane, again))
+            use(x, again);
+          __syncwarp();
+        }
+      };
       float* lse = nullptr;
       if (p.lse && r < rows) {
         const int tok = div_group(p, rbase + r), hd = cur.head * p.group + rbase + r - tok * p.group;
@@ -552,12 +589,20 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
             uint32_t o[32];
             tld<32>(o_tm + 64 * ch + 32 * h, o);
             tld_wait<32>(o);
+            look(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               w[16 * h + i] = pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
           }
           put_out(cur, rows, 64 * ch, w);
         }
+        redo([&](int x, const float* again) {
+          const float f = __shfl_sync(0xffffffffu, l, x) == 0.f ? 0.f : 1.f / __shfl_sync(0xffffffffu, l, x);
+          const int rr = rbase + (warp & 3) * 32 + x, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
+          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = __float2bfloat16_rn(again[i] * f);
+        });
         if (lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       } else {
         // partial result: columns in groups of four, the rows of a group side by side
@@ -568,6 +613,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
           uint32_t o[32];
           tld<32>(o_tm + 32 * ch, o);
           tld_wait<32>(o);
+          look(o);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(reinterpret_cast<uint4*>(slot) + (8 * ch + i) * C::RB + at,
@@ -575,15 +621,27 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         }
         __stcg(slot + C::RB * D + at, m);
         __stcg(slot + C::RB * (D + 1) + at, l);
+        __syncwarp();
+        redo([&](int x, const float* again) {
+          const int row = 128 * rt + (warp & 3) * 32 + x;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int d = lane * (D / 32) + i;
+            __stcg(slot + ((d >> 2) * C::RB + row) * 4 + (d & 3), again[i] / left_in(TYPE));
+          }
+        });
         // each warp joins its own 32 rows: the last CTA's warp to come, in the parts' order
         uint32_t* counter = p.counters + 8 * ca + warp;
-        __threadfence();
         __syncwarp();
         int is_last = 0;
-        if (lane == 0) is_last = atomicAdd(counter, 1u) == (uint32_t)(cb - ca);
-        if (__shfl_sync(0xffffffffu, is_last, 0)) {
+        if (lane == 0) {  // with the warp's barriers, one lane's fences order all its accesses
           __threadfence();
-          if (lane == 0) *counter = 0u;
+          is_last = atomicAdd(counter, 1u) == (uint32_t)(cb - ca);
+          if (is_last) *counter = 0u;
+          __threadfence();
+        }
+        if (__shfl_sync(0xffffffffu, is_last, 0)) {
+          __syncwarp();
           auto part = [&](int x) { return p.partials + (size_t)(2 * x + (x == ca ? 1 : 0)) * C::slot_floats; };
           float mm = -INFINITY, ll = 0.f;
 #pragma unroll 8

@@ -23,6 +23,7 @@
 // are rarely rescaled.
 #pragma once
 
+#include "ft_attn_redo.cuh"
 #include "ft_kv_internal.cuh"
 
 namespace ft {
@@ -85,11 +86,6 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -99,26 +95,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Two E4M3 codes in the high bytes of both halves -> the BF16 numbers they stand for, times 2^-120.
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) { return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u); }
-// Nibble I of both halves -> the BF16 numbers their E2M1 codes stand for, times 2^-126.
-template <int I>
-__device__ __forceinline__ uint32_t e2m1_bits(uint32_t w) {
-  const uint32_t mag = I == 0 ? w << 6 : I == 1 ? w << 2 : I == 2 ? w >> 2 : w >> 6;
-  const uint32_t sgn = w << (12 - 4 * I);
-  return (mag & 0x01C001C0u) | (sgn & 0x80008000u);
-}
-
-// Scale codes in the high bytes of both halves -> BF16 multipliers: 2^e times what the codes'
-// bits lack.  A code above 134 (MXFP8) or 144 (MXFP4) gives infinity, which makes the zero
-// codes of a NaN block NaN.
-template <int TYPE>
-__device__ __forceinline__ uint32_t multiplier(uint32_t t) {
-  constexpr uint32_t lack = TYPE == FT_KV_MXFP8 ? 0x7B807B80u   // 2^120
-                                                : 0x76807680u;  // 2^110: 2^-16 is left in
-  return mul2(t >> 1, lack);
 }
 
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -157,7 +133,7 @@ struct Cfg {
   static constexpr int CHUNK = q && D <= 128 ? 32 : 16;
   static constexpr int UT = CHUNK * kWarps;          // tokens of a tile
   static constexpr int OV = CHUNK == 32 ? 2 : 4;     // counts of an item besides its tiles
-  static constexpr int least = CHUNK == 32 ? 1 : 2;  // counts of a CTA's share, at least
+  static constexpr float join_cost = 0.35f;          // tiles' time that a part of an item costs the join
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
@@ -234,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
   pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
   Walk<RB, UT, C::OV> wk;
   long long per;
-  if (!plan<RB, UT, C::OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), C::least, wk, per)) return;
+  if (!plan<RB, UT, C::OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), C::join_cost, wk, per)) return;
   __syncthreads();
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;
@@ -409,9 +385,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       const uint32_t st = ring + (uint32_t)(k % S) * C::stage;
       float ve = 0.f;
       if constexpr (C::q) {
-        // The chunk's scale codes as FP32 powers of two (255: infinity, which makes the zero codes
-        // of its block NaN), zero for tokens that are left out; and log2 of the largest one of
-        // the values, 13 at most.
+        // The chunk's scale codes as FP32 powers of two, zero for tokens that are left out; and
+        // log2 of the largest one of the values, 13 at most.
         const uint8_t* codes = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
         // Lane l takes the codes of token l % CHUNK: with 16 tokens of K or of V, with 32 of both.
         constexpr int SETS = CHUNK / 16;
@@ -432,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t code = (w[b >> 2] >> (8 * (b & 3))) & 0xffu;
-            sc_f[(set * NB + b) * CHUNK + tok] = __uint_as_float(in ? code << 23 : 0u);
+            sc_f[(set * NB + b) * CHUNK + tok] = in ? e8m0(code) : 0.f;
             if (set == 1) top = max(top, in && code < 255u ? code : 0u);
           }
         }
@@ -452,6 +427,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         for (int i = 0; i < 4 * TT; ++i) s[mt][i >> 2][i & 3] = 0.f;
       const int mrow = (lane & 7) + ((lane >> 4) << 3), mpc = (lane >> 3) & 1;  // ldmatrix row and piece of this lane
       if constexpr (!C::q) {
+        float s2[MT][TT][4];  // even and odd steps apart: each product waits for the one before last
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4 * TT; ++i) s2[mt][i >> 2][i & 3] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t b[4], a[4];
@@ -459,10 +439,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             query(mt, ks, a);
-            mma(s[mt][0], a, b[0], b[1]);
-            mma(s[mt][1], a, b[2], b[3]);
+            mma(ks & 1 ? s2[mt][0] : s[mt][0], a, b[0], b[1]);
+            mma(ks & 1 ? s2[mt][1] : s[mt][1], a, b[2], b[3]);
           }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4 * TT; ++i) s[mt][i >> 2][i & 3] += s2[mt][i >> 2][i & 3];
       } else {
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {  // a 1x32 block: two k steps
@@ -676,6 +660,31 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         acc[i].w += v.w * wt[x];
       }
     }
+    {  // sums that are not finite: because of values that the row does not see?
+      float bad = 0.f;
+#pragma unroll
+      for (int i = 0; i < PC; ++i) bad = fmaf(acc[i].x, 0.f, fmaf(acc[i].y, 0.f, fmaf(acc[i].z, 0.f, fmaf(acc[i].w, 0.f, bad))));
+      uint32_t rows_bad = __ballot_sync(0xffffffffu, bad != bad && r < rows);
+      const int a = max((cur.t0 + ta) * UT, cur.lo), b = min((cur.t0 + tb) * UT, cur.hi);  // the part's tokens
+      while (rows_bad) {
+        const int leader = (__ffs(rows_bad) - 1) / TPR * TPR;  // the row's first thread
+        rows_bad &= ~(((TPR == 32 ? 0u : 1u << TPR) - 1u) << leader);
+        const int row = (warp * 32 + leader) / TPR, pos = cur.len - cur.n + div_group(p, cur.rb * RB + row);
+        const int see_hi = p.causal ? min(cur.len, pos + 1) : cur.len, see_lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+        if (see_lo <= a && see_hi >= b) continue;
+        float again[D / 32];
+        const float m_row = __shfl_sync(0xffffffffu, mm, leader);
+        if (!redo_row<TYPE, D>(p, cur, cur.rb * RB + row, see_lo, see_hi, a, b, m_row, lane, again)) continue;
+        float* to = join_o + row * C::opitch;  // the row's sums have been taken from here
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = again[i];
+        __syncwarp();
+        if (r == row)
+#pragma unroll
+          for (int i = 0; i < PC; ++i) acc[i] = *reinterpret_cast<const float4*>(to + 4 * (sub + TPR * i));
+        __syncwarp();
+      }
+    }
     auto put = [&](int row, int piece4, float4 v, float inv) {
       const int rr = cur.rb * RB + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
       *reinterpret_cast<uint2*>(p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D + 4 * piece4) =
@@ -706,14 +715,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           __stcg(slot + RB * D + RB + r, ll);
         }
       }
-      __threadfence();
       __syncthreads();
-      if (tid == 0) *s_flag = atomicAdd(p.counters + first, 1u) == (uint32_t)(last - first);
+      if (tid == 0) {  // the barrier and one thread's fences order the whole block's accesses
+        __threadfence();
+        const bool is_last = atomicAdd(p.counters + first, 1u) == (uint32_t)(last - first);
+        if (is_last) p.counters[first] = 0u;
+        __threadfence();
+        *s_flag = is_last;
+      }
       __syncthreads();
       if (*s_flag) {
         // the last one: join the item's parts in their order
-        __threadfence();
-        if (tid == 0) p.counters[first] = 0u;
         auto part = [&](int x) { return p.partials + (size_t)(2 * x + (x == first ? 1 : 0)) * C::slot_floats; };
         float* weight = reinterpret_cast<float*>(body);  // [parts][RB]
         const int np = last - first + 1;

@@ -28,6 +28,9 @@ __host__ __device__ constexpr int scale_bytes(int type, int D) { return type == 
 // scale, so 2^-16 is left in (the attention takes it out of its scores and sums in FP32).
 __host__ __device__ constexpr float left_in(int type) { return type == FT_KV_MXFP4 ? 65536.f : 1.f; }
 
+// The power of two of an E8M0 code, NaN for code 255.
+__device__ __forceinline__ float e8m0(uint32_t code) { return __uint_as_float(code << 23 | (code + 1) >> 8); }
+
 inline int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
 
 // Sets a kernel's shared-memory limit on the current device, once.  All of these kernels ask
@@ -208,21 +211,30 @@ struct PlanSmem {
   long long part[33];
   Cursor cur;
   long long total;
-  int n_many, found;
+  int n_many, found, longest;
 };
 
+// Counts of a share: the total over the CTAs, but no less than suits the longest item.  An item
+// of c tiles cut into n parts takes c / n tiles' time, and then joining the parts takes n times
+// what a part costs, `join` tiles: the sum is least for parts of sqrt(c * join) tiles.  Up to
+// three tiles are not worth a second part.
+__device__ __forceinline__ long long share(long long total, int longest, float join) {
+  return max(quotient(total + gridDim.x - 1, gridDim.x), (long long)max((int)ceilf(sqrtf((float)longest * join)), 3));
+}
+
 // All NT threads of the block (a multiple of 32) find the CTA's share and its first item.
-// per: counts of a share, at least `least`.  Returns false for a CTA without work.  Counts are
-// summed for one head and multiplied by the heads at the end.
+// per: counts of a share.  Returns false for a CTA without work.  Counts are summed for one head
+// and multiplied by the heads at the end.
 template <int RB, int UT, int OV, int NT>
-__device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, OV>& wk, long long& per) {
+__device__ bool plan(const AttnParams& p, PlanSmem& sm, float join, Walk<RB, UT, OV>& wk, long long& per) {
   constexpr int kFew = 4;    // blocks of a sequence that one thread counts
   constexpr int kStrips = 4; // sequences / 32 that a warp counts by itself
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (p.n_seqs <= 32 * kStrips) {
+  if (p.n_seqs <= 32 * kStrips && (p.table_stride << p.page_shift) / UT < 1 << 20) {  // sums below 2^31
     // Few sequences of few blocks each, as in decode: every warp counts them all, and nothing
     // waits for another warp.
     int sum[kStrips], q0, n, len;
+    int longest = 0;
     bool alone = true, any_bad = false;
 #pragma unroll
     for (int i = 0; i < kStrips; ++i) {
@@ -238,19 +250,20 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
           int lo, hi, t0, cost;
           block_range<RB, UT>(p, b, n, len, lo, hi, t0, cost);
           sum[i] += cost + OV;
+          longest = max(longest, cost);
         }
       }
     }
     if (__all_sync(0xffffffffu, alone)) {
       if (any_bad && blockIdx.x == 0 && warp == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
-      long long before[kStrips], run = 0;  // counts of one head before a strip's sequences
+      int before[kStrips], run = 0;  // counts of one head before a strip's sequences
 #pragma unroll
       for (int i = 0; i < kStrips; ++i) {
         if (32 * i < p.n_seqs) {
-          long long x = sum[i];
+          int x = sum[i];
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
           }
           before[i] = run + x - sum[i];
@@ -259,14 +272,14 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
           before[i] = run;
         }
       }
-      const long long total = run * p.n_kv_heads;
-      per = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
+      const long long total = (long long)run * p.n_kv_heads;
+      per = share(total, (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest), join);
       wk.w = per * blockIdx.x;
       wk.w1 = min(wk.w + per, total);
       if (wk.w >= wk.w1) return false;
-      const long long at = quotient(wk.w, p.n_kv_heads);
+      const int at = (int)quotient(wk.w, p.n_kv_heads);
       Cursor& c = wk.cur;
-      long long base = 0;
+      int base = 0;
 #pragma unroll
       for (int i = 0; i < kStrips; ++i) {
         const uint32_t hit = __ballot_sync(0xffffffffu, before[i] <= at && at < before[i] + sum[i]);
@@ -282,16 +295,17 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
         if (at < base + c.cost + OV) break;
         base += c.cost + OV;
       }
-      const long long first = base * p.n_kv_heads;
+      const long long first = (long long)base * p.n_kv_heads;
       c.head = (int)quotient(wk.w - first, c.cost + OV);
       c.start = first + (long long)c.head * (c.cost + OV);
       if (wk.w >= wk.end()) wk.next_item(p);
       return wk.more();
     }
   }
-  if (tid == 0) sm.n_many = 0;
+  if (tid == 0) sm.n_many = sm.longest = 0;
   __syncthreads();
   bool any_bad = false;
+  int longest = 0;
   for (int s = tid; s < p.n_seqs; s += NT) {
     int q0, n, len;
     bool bad;
@@ -299,6 +313,11 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
     any_bad |= bad;
     const int nb = row_blocks<RB>(n, p.group);
     long long sum = 0;
+    if (nb > 0) {
+      int lo, hi, t0, cost;
+      block_range<RB, UT>(p, nb - 1, n, len, lo, hi, t0, cost);  // no block sees more than the last
+      longest = max(longest, cost);
+    }
     if (nb <= kFew) {
       for (int b = 0; b < nb; ++b) {
         int lo, hi, t0, cost;
@@ -311,6 +330,8 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
     sm.sum[s] = sum;
   }
   if (any_bad && blockIdx.x == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
+  longest = (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest);
+  if (lane == 0) atomicMax(&sm.longest, longest);
   __syncthreads();
   // sequences of many blocks: several warps count a slice of one each, or a warp several of them
   const int n_many = sm.n_many;
@@ -354,7 +375,7 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, int least, Walk<RB, UT, 
   }
   __syncthreads();
   const long long one_head = sm.total, total = one_head * p.n_kv_heads;
-  per = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
+  per = share(total, sm.longest, join);
   const long long w0 = per * blockIdx.x;
   wk.w = w0;
   wk.w1 = min(w0 + per, total);

@@ -122,8 +122,7 @@ __device__ __forceinline__ uint8_t quantise(const uint4* in, uint4* codes) {
 // What a block's codes and scale stand for, as 32 BF16 values.
 template <int TYPE>
 __device__ __forceinline__ void stands_for(const uint4* codes, uint32_t scale, uint4* out) {
-  // 2^e in FP32; code 255 is infinity here, and a NaN block's codes are zero: 0 * inf is NaN
-  const float s = __uint_as_float(scale << 23);
+  const float s = e8m0(scale);
   const uint32_t in[8] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w,
                           TYPE == FT_KV_MXFP8 ? codes[1].x : 0, TYPE == FT_KV_MXFP8 ? codes[1].y : 0,
                           TYPE == FT_KV_MXFP8 ? codes[1].z : 0, TYPE == FT_KV_MXFP8 ? codes[1].w : 0};

@@ -310,3 +310,29 @@ def test_kernels_for_few_and_for_many_rows_agree(F, kind, heads, kv_heads, dim, 
     tol = 2.0 ** -8 * np.abs(o1) + (2.0 ** -8 + 2 * d + 2.0 ** -20) * v
     assert np.all(np.abs(o1 - o2) <= 2 * tol)
     assert np.all(np.abs(l1 - l2) <= 2 * (d + 2.0 ** -20 * (1 + np.abs(l1))))
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim,new,length,window", [
+    (4, 2, 64, 4, 300, 0), (8, 1, 128, 2, 70, 33), (7, 1, 128, 4, 2000, 0), (4, 2, 256, 3, 45, 0),   # few rows
+    (4, 1, 64, 140, 400, 50), (8, 1, 128, 60, 200, 0), (16, 2, 256, 40, 130, 0), (8, 1, 128, 300, 1500, 0)])  # chunks
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_values_that_a_row_does_not_see_do_not_matter(F, kind, heads, kv_heads, dim, new, length, window, value):
+    """A cached token within the chunk has values (and keys) that are not finite: rows before it, and rows whose window has
+    left it behind, are as if it were not there; rows that see it are NaN."""
+    b = Batch(F, kind, heads, kv_heads, dim, 16, new=[new, 1], lens=[length, 40], window=window)
+    at = length - new + new // 2  # seen by the later half of the new tokens
+    page, off = int(b.table[0, at // 16]), at % 16
+    for h in range(kv_heads):
+        b.cache.poison(0, page, h, off)
+        if kind == 0 and value == "inf":
+            b.cache.t[1][page, h, off] = float("inf")
+        else:
+            b.cache.poison(1, page, h, off)
+        b.cache.value[1][page, h, off] = 0.0  # for the rows that do not see it
+        b.cache.value[0][page, h, off] = 0.0
+    def sees(s, i):
+        return s == 0 and length - new + i >= at and (not window or at > length - new + i - window)
+    out, lse = b.check(rows=lambda s, i: not sees(s, i))
+    seeing = [i for i in range(new) if sees(0, i)]
+    assert seeing and np.all(np.isnan(out[seeing])) and np.all(np.isnan(lse[seeing]))
