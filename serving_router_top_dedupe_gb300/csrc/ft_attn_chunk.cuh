@@ -33,7 +33,6 @@ using rows::pack;
 constexpr int KT = 128;           // cached tokens of a tile
 constexpr int PANEL = KT * 128;   // bytes of 64 columns of a tile: rows of 128 bytes, 128-byte swizzle
 constexpr float kJoin = 1.2f;     // tiles' time that a part of an item costs the join
-constexpr int OV = 2;             // counts of an item besides its tiles
 constexpr float kSlack = 8.f;     // log2 units by which scores may pass the running maximum
 
 template <int TYPE, int D>
@@ -41,6 +40,7 @@ struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
   static constexpr int tiles = D <= 128 ? 2 : 1;
   static constexpr int RB = 128 * tiles;
+  static constexpr int OV = D == 64 ? 5 : 3;  // counts of an item besides its tiles
   static constexpr int panels = D / 64;
   static constexpr int stage = panels * PANEL;
   static constexpr int stages = D == 64 ? 4 : D == 128 ? 2 : 1;  // of K, and of V
@@ -164,7 +164,7 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int 
 }
 
 template <int TYPE, int D>
-using ChunkWalk = Walk<Cfg<TYPE, D>::RB, KT, OV>;
+using ChunkWalk = Walk<Cfg<TYPE, D>::RB, KT, Cfg<TYPE, D>::OV>;
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   if (p.have && __ldg(p.have) != p.want) return;
   ChunkWalk<TYPE, D> wk;
   long long per;
-  if (!plan<C::RB, KT, OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kJoin, wk, per)) return;
+  if (!plan<C::RB, KT, C::OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), kJoin, wk, per)) return;
   if (warp == C::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(tmem_slot))
                  : "memory");

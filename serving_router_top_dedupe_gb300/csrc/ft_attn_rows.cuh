@@ -132,7 +132,7 @@ struct Cfg {
   // is long for decoding; 256-wide heads have no registers for that.
   static constexpr int CHUNK = q && D <= 128 ? 32 : 16;
   static constexpr int UT = CHUNK * kWarps;          // tokens of a tile
-  static constexpr int OV = CHUNK == 32 ? 2 : 4;     // counts of an item besides its tiles
+  static constexpr int OV = CHUNK == 32 ? 3 : 6;     // counts of an item besides its tiles
   static constexpr float join_cost = 0.35f;          // tiles' time that a part of an item costs the join
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;

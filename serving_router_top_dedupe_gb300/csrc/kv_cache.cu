@@ -1,10 +1,10 @@
-// Paged key/value cache: writing new tokens' rows (quantised on the way) and gathering cached
-// rows, plus the argument checks of the cache's entry points.
+// Paged key/value cache: writing new tokens' rows (quantised on the way), gathering cached rows,
+// and decoding whole pages, plus the argument checks of the cache's entry points.
 //
-// Both kernels move each byte once and compute next to nothing, so memory bounds them.  One
-// thread takes one 1x32 block (BF16 input 64 bytes, in four 16-byte loads), which makes the
-// block's maximum a matter of one thread and its stores 32 or 16 bytes wide; a block's
-// neighbours in a warp are its row's, so a warp's accesses cover whole rows.
+// These kernels move each byte once and compute next to nothing, so memory bounds them.  A
+// thread takes eight neighbouring elements, 16 bytes of BF16, so that every access of a warp
+// covers whole lines; the four threads of a 1x32 block find its maximum with two shuffles.
+// With much to move, a thread takes four such pieces, so that enough loads are under way.
 #include <cstdarg>
 #include <cstdio>
 
@@ -82,65 +82,64 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* f) {
   return r;
 }
 
-// Block of 32 BF16 values -> 32 or 16 bytes of codes and the scale code.
+// Eight BF16 values of a thread, of the block that its group of four lanes holds -> their codes
+// (8 or 4 bytes) and the block's scale code.
 template <int TYPE>
-__device__ __forceinline__ uint8_t quantise(const uint4* in, uint4* codes) {
-  uint32_t w[16];
+__device__ __forceinline__ uint32_t quantise(const uint4 in, uint2& codes) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  uint32_t top = 0;  // of the magnitudes
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool nan = top >= 0x7f80u;  // a NaN or an infinity: the whole block reads back as NaN
+  const int e = block_exponent<TYPE>(top << 16);
+  const float inv = nan ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+  float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[4 * i] = in[i].x;
-    w[4 * i + 1] = in[i].y;
-    w[4 * i + 2] = in[i].z;
-    w[4 * i + 3] = in[i].w;
-  }
-  uint32_t top = 0;  // of the magnitudes, as 16-bit patterns in both halves
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-  const uint32_t a = max(top >> 16, top & 0xffffu) << 16;
-  const bool nan = a >= 0x7f800000u;  // a NaN or an infinity: the whole block reads back as NaN
-  const int e = block_exponent<TYPE>(a);
-  const float inv = nan ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
     f[2 * i] = __uint_as_float(w[i] << 16) * inv;
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
   }
-  uint32_t c[8];
   if (TYPE == FT_KV_MXFP8) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = nan ? 0u : e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    codes[1] = make_uint4(c[4], c[5], c[6], c[7]);
+    codes.x = nan ? 0u : e4m3x4(f[0], f[1], f[2], f[3]);
+    codes.y = nan ? 0u : e4m3x4(f[4], f[5], f[6], f[7]);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = nan ? 0u : e2m1x8(f + 8 * i);
+    codes.x = nan ? 0u : e2m1x8(f);
   }
-  codes[0] = make_uint4(c[0], c[1], c[2], c[3]);
-  return nan ? 255 : (uint8_t)(e + 127);
+  return nan ? 255u : (uint32_t)(e + 127);
 }
 
-// What a block's codes and scale stand for, as 32 BF16 values.
+// What eight codes and their scale stand for, as BF16.
 template <int TYPE>
-__device__ __forceinline__ void stands_for(const uint4* codes, uint32_t scale, uint4* out) {
+__device__ __forceinline__ uint4 stands_for(const uint2 codes, uint32_t scale) {
   const float s = e8m0(scale);
-  const uint32_t in[8] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w,
-                          TYPE == FT_KV_MXFP8 ? codes[1].x : 0, TYPE == FT_KV_MXFP8 ? codes[1].y : 0,
-                          TYPE == FT_KV_MXFP8 ? codes[1].z : 0, TYPE == FT_KV_MXFP8 ? codes[1].w : 0};
-  uint32_t o[16];
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 4; ++i) {
     float2 f;
     if (TYPE == FT_KV_MXFP8) {
-      f = dot::e4m3x2_to_float2((uint16_t)(in[i / 2] >> (16 * (i & 1))));
+      f = dot::e4m3x2_to_float2((uint16_t)((i < 2 ? codes.x : codes.y) >> (16 * (i & 1))));
     } else {
-      const uint32_t h2 = dot::e2m1x2_to_f16x2((in[i / 4] >> (8 * (i & 3))) & 0xffu);
+      const uint32_t h2 = dot::e2m1x2_to_f16x2((codes.x >> (8 * i)) & 0xffu);
       f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
     }
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);  // exact
     o[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight elements' codes from and to memory: 8 or 4 bytes.
+template <int TYPE>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p) {
+  if (TYPE == FT_KV_MXFP8) return __ldg(reinterpret_cast<const uint2*>(p));
+  return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), 0u);
+}
+template <int TYPE>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c) {
+  if (TYPE == FT_KV_MXFP8) *reinterpret_cast<uint2*>(p) = c;
+  else *reinterpret_cast<uint32_t*>(p) = c.x;
 }
 
 // Slot of token t: >= 0, or -1 for a row that is not there.
@@ -151,61 +150,72 @@ __device__ __forceinline__ int slot_of(const RowsParams& p, int t) {
   return -1;
 }
 
-// Thread = one block of 32 elements of a row of K (blockIdx.y 0) or V (1).
-template <int TYPE, int D, bool WRITE>
+// Eight elements of a row of K (blockIdx.y 0) or V (1), EACH times.  Rows have a multiple of 32
+// elements, so the four lanes of a block are together always.
+template <int TYPE, int D, bool WRITE, int EACH>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsParams p) {
-  constexpr int NB = D / 32;
+  constexpr int NP = D / 8;  // pieces of a row
   pdl_wait();
   pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const int per = p.n_kv_heads * NB;
-  const int t = (int)(i / per);
-  if (t >= p.n_tokens) return;
-  const int r = (int)(i - (long long)t * per), head = r / NB, b = r % NB;
   const bool is_v = blockIdx.y != 0;
-  const int slot = slot_of(p, t);
-  const long long dense = (long long)t * (is_v ? p.v_stride : p.k_stride) + head * D + b * 32;
-  const long long row = (((long long)(slot >> p.page_shift) * p.n_kv_heads + head) << p.page_shift) +
-                        (slot & (p.page_size - 1));
-  uint4* codes = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + row * row_bytes(TYPE, D) + b * row_bytes(TYPE, 32));
-  uint8_t* scale = TYPE == FT_KV_BF16 ? nullptr : (is_v ? p.vs : p.ks) + row * NB + b;
-  uint4 x[4];
-  if (WRITE) {
-    if (slot < 0) return;
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_in : p.k_in) + dense);
+  const long long i0 = (long long)blockIdx.x * (kThreads * EACH) + threadIdx.x;
+  const uint32_t per = (uint32_t)p.n_kv_heads * NP;
+  uint8_t* const codes = is_v ? p.v : p.k;
+  uint8_t* const scales = is_v ? p.vs : p.ks;
+  int slot[EACH];
+  long long dense[EACH], row[EACH];
+  int d[EACH];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __ldg(src + j);
-    if constexpr (TYPE == FT_KV_BF16) {
+  for (int e = 0; e < EACH; ++e) {
+    const long long i = i0 + e * kThreads;
+    const long long t = (i >> 32) == 0 ? (long long)((uint32_t)i / per) : i / per;
+    const uint32_t r = (uint32_t)(i - t * per), head = r / NP;
+    d[e] = (r % NP) * 8;
+    slot[e] = t < p.n_tokens ? slot_of(p, (int)t) : -2;  // -1: padding, -2: no such token
+    dense[e] = t * (is_v ? p.v_stride : p.k_stride) + head * D + d[e];
+    row[e] = (((long long)(slot[e] >> p.page_shift) * p.n_kv_heads + head) << p.page_shift) + (slot[e] & (p.page_size - 1));
+  }
+  uint4 x[EACH];
+  uint2 c[EACH];
+  uint32_t sc[EACH];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) codes[j] = x[j];
+  for (int e = 0; e < EACH; ++e) {
+    x[e] = make_uint4(0, 0, 0, 0);
+    c[e] = make_uint2(0, 0);
+    sc[e] = 0;
+    if (slot[e] < 0) continue;
+    if (WRITE) {
+      x[e] = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v_in : p.k_in) + dense[e]));
+    } else if (TYPE == FT_KV_BF16) {
+      x[e] = __ldg(reinterpret_cast<const uint4*>(codes + (row[e] * D + d[e]) * 2));
     } else {
-      uint4 c[2];
-      *scale = quantise<TYPE>(x, c);
-      codes[0] = c[0];
-      if (TYPE == FT_KV_MXFP8) codes[1] = c[1];
+      c[e] = load_codes<TYPE>(codes + row[e] * row_bytes(TYPE, D) + d[e] * row_bytes(TYPE, 8) / 8);
+      sc[e] = __ldg(scales + row[e] * (D / 32) + d[e] / 32);
     }
-  } else {
-    if (slot < 0) {
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = make_uint4(0, 0, 0, 0);
-    } else if constexpr (TYPE == FT_KV_BF16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = codes[j];
+  for (int e = 0; e < EACH; ++e) {
+    if (WRITE) {
+      uint32_t scale = 0;
+      if constexpr (TYPE != FT_KV_BF16) scale = quantise<TYPE>(x[e], c[e]);  // every lane takes part
+      if (slot[e] < 0) continue;
+      if constexpr (TYPE == FT_KV_BF16) {
+        *reinterpret_cast<uint4*>(codes + (row[e] * D + d[e]) * 2) = x[e];
+      } else {
+        store_codes<TYPE>(codes + row[e] * row_bytes(TYPE, D) + d[e] * row_bytes(TYPE, 8) / 8, c[e]);
+        if (d[e] % 32 == 0) scales[row[e] * (D / 32) + d[e] / 32] = (uint8_t)scale;
+      }
     } else {
-      uint4 c[2];
-      c[0] = codes[0];
-      if (TYPE == FT_KV_MXFP8) c[1] = codes[1];
-      stands_for<TYPE>(c, *scale, x);
+      if (slot[e] == -2) continue;
+      if constexpr (TYPE != FT_KV_BF16)
+        if (slot[e] >= 0) x[e] = stands_for<TYPE>(c[e], sc[e]);
+      *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + dense[e]) = x[e];
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + dense);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dst[j] = x[j];
   }
 }
 
 // Decodes every page that a batch's new tokens may see, once, into a BF16 copy.  One warp takes
-// one page of one head, of K (blockIdx.y 0) or V; lanes take 1x32 blocks, so that a warp reads
-// and writes whole lines.  Reading the codes and writing twice or four times their bytes bounds
+// one page of one head, of K (blockIdx.y 0) or V, in pieces of eight elements.  Reading the codes and writing twice or four times their bytes bounds
 // it.
 constexpr int kStageThreads = 256;
 
@@ -291,28 +301,35 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageParams 
     if (!ok && lane == 0) atomicOr(a.error_word, FT_DEVERR_BAD_INDEX);
     const long long from = ((long long)(ok ? page : 0) * a.n_kv_heads + head) << a.page_shift;
     const long long to = ((long long)sp * a.n_kv_heads + head) << a.page_shift;
-    for (int b = lane; b < a.page_size * NB; b += 32) {
-      uint4 c[2], y[4];
-      const uint4* codes = reinterpret_cast<const uint4*>(codes0 + from * row_bytes(TYPE, D) + b * row_bytes(TYPE, 32));
-      c[0] = __ldg(codes);
-      if (TYPE == FT_KV_MXFP8) c[1] = __ldg(codes + 1);
-      const uint32_t scale = ok ? __ldg(scales0 + from * NB + b) : 0u;
-      stands_for<TYPE>(c, scale, y);
-      if (!ok) y[0] = y[1] = y[2] = y[3] = make_uint4(0, 0, 0, 0);
-      uint4* dst = reinterpret_cast<uint4*>(out0 + to * D + b * 32);
+    const uint8_t* codes = codes0 + from * row_bytes(TYPE, D);
+    const uint8_t* scales = scales0 + from * NB;
+    uint4* dst = reinterpret_cast<uint4*>(out0 + to * D);
+    // pieces of eight elements: a multiple of 128 in a page
+    for (int b = lane; b < a.page_size * (D / 8); b += 128) {
+      uint2 c[4];
+      uint32_t sc[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = y[i];
+      for (int i = 0; i < 4; ++i) {
+        c[i] = load_codes<TYPE>(codes + (b + 32 * i) * row_bytes(TYPE, 8));
+        sc[i] = __ldg(scales + (b + 32 * i) / 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[b + 32 * i] = ok ? stands_for<TYPE>(c[i], sc[i]) : make_uint4(0, 0, 0, 0);
     }
   }
 }
 
 template <int TYPE, int D>
 cudaError_t launch_rows_t(const RowsParams& p, bool write, cudaStream_t s) {
-  const long long threads = (long long)p.n_tokens * p.n_kv_heads * (D / 32);
-  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
-  static std::atomic<uint64_t> ready[2];
-  const auto kernel = write ? rows_kernel<TYPE, D, true> : rows_kernel<TYPE, D, false>;
-  const cudaError_t e = prepare_kernel(kernel, 0, ready[write]);
+  const long long pieces = (long long)p.n_tokens * p.n_kv_heads * (D / 8);
+  // one piece a thread while that fills the GPU's threads no more than about once
+  const bool much = pieces > 1 << 17;
+  const int each = kThreads * (much ? 4 : 1);
+  const dim3 grid((unsigned)((pieces + each - 1) / each), 2);
+  static std::atomic<uint64_t> ready[4];
+  const auto kernel = write ? (much ? rows_kernel<TYPE, D, true, 4> : rows_kernel<TYPE, D, true, 1>)
+                            : (much ? rows_kernel<TYPE, D, false, 4> : rows_kernel<TYPE, D, false, 1>);
+  const cudaError_t e = prepare_kernel(kernel, 0, ready[2 * write + much]);
   return e == cudaSuccess ? launch_k(kernel, grid, dim3(kThreads), 0, s, true, p) : e;
 }
 
