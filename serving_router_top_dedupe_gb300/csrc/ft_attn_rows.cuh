@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
   pdl_trigger();  // the next launch may take its place; it waits for this one's end before it reads
   Walk<RB, UT, C::OV> wk;
   long long per;
-  if (!plan<RB, UT, C::OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), C::join_cost, wk, per)) return;
+  if (!plan<RB, UT, C::OV, kThreads>(p, *reinterpret_cast<PlanSmem*>(body), blockIdx.x, gridDim.x, C::join_cost, wk, per)) return;
   __syncthreads();
 
   const uint32_t ring = smem_addr(body) + warp * S * C::stage;

@@ -218,15 +218,16 @@ struct PlanSmem {
 // of c tiles cut into n parts takes c / n tiles' time, and then joining the parts takes n times
 // what a part costs, `join` tiles: the sum is least for parts of sqrt(c * join) tiles.  Up to
 // three tiles are not worth a second part.
-__device__ __forceinline__ long long share(long long total, int longest, float join) {
-  return max(quotient(total + gridDim.x - 1, gridDim.x), (long long)max((int)ceilf(sqrtf((float)longest * join)), 3));
+__device__ __forceinline__ long long share(long long total, int ctas, int longest, float join) {
+  return max(quotient(total + ctas - 1, ctas), (long long)max((int)ceilf(sqrtf((float)longest * join)), 3));
 }
 
-// All NT threads of the block (a multiple of 32) find the CTA's share and its first item.
+// All NT threads of the block (a multiple of 32) find the share of CTA `cta` of `ctas` and its first item.
 // per: counts of a share.  Returns false for a CTA without work.  Counts are summed for one head
 // and multiplied by the heads at the end.
 template <int RB, int UT, int OV, int NT>
-__device__ bool plan(const AttnParams& p, PlanSmem& sm, float join, Walk<RB, UT, OV>& wk, long long& per) {
+__device__ bool plan(const AttnParams& p, PlanSmem& sm, int cta, int ctas, float join, Walk<RB, UT, OV>& wk,
+                     long long& per) {
   constexpr int kFew = 4;    // blocks of a sequence that one thread counts
   constexpr int kStrips = 4; // sequences / 32 that a warp counts by itself
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -273,8 +274,8 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, float join, Walk<RB, UT,
         }
       }
       const long long total = (long long)run * p.n_kv_heads;
-      per = share(total, (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest), join);
-      wk.w = per * blockIdx.x;
+      per = share(total, ctas, (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest), join);
+      wk.w = per * cta;
       wk.w1 = min(wk.w + per, total);
       if (wk.w >= wk.w1) return false;
       const int at = (int)quotient(wk.w, p.n_kv_heads);
@@ -375,8 +376,8 @@ __device__ bool plan(const AttnParams& p, PlanSmem& sm, float join, Walk<RB, UT,
   }
   __syncthreads();
   const long long one_head = sm.total, total = one_head * p.n_kv_heads;
-  per = share(total, sm.longest, join);
-  const long long w0 = per * blockIdx.x;
+  per = share(total, ctas, sm.longest, join);
+  const long long w0 = per * cta;
   wk.w = w0;
   wk.w1 = min(w0 + per, total);
   if (w0 >= wk.w1) return false;
