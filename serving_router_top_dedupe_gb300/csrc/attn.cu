@@ -1,4 +1,5 @@
 // ft_attn: argument checks, workspace and the choice of the kernel.
+#include <algorithm>
 #include <cmath>
 
 #include "ft_kv_internal.cuh"
@@ -40,10 +41,40 @@ size_t workspace_least(int n_sm, int D) { return kCounterBytes + 256 + partial_b
 constexpr size_t kStageHead = kMaxSeqs * 4 + 256;
 constexpr size_t kStageBytes = (size_t)512 << 20;
 
-// The decoded copy costs reading the codes and writing 4 bytes per pair of elements once; without
-// it every block of rows decodes what it reads.  For 2048 rows of a head over 16384 tokens
-// ... the two meet near four blocks.
+// From this many rows of a head on, a quantised cache's pages are decoded once into a BF16 copy;
+// below it each block of 256 rows decodes what it reads.  Both sides measured (us, 16 query heads
+// over 4 cache heads of 128, 65536 cached tokens): MXFP8 512 rows 165 direct, 158 copied; 1024:
+// 240 and 195; 2048: 406 and 296.  MXFP4 512 rows 130 and 150; 1024: 179 and 185; 2048: 301 and 288.
 constexpr int kStageRows = 1024;
+
+// Whether the few-row kernel takes a batch (rows: of one cache head of a sequence, at most).  It
+// re-reads the cache for every 16 or 32 rows; the chunk kernel does so for every 256, but takes
+// 12 us longer to start and to end, and decodes a quantised cache's tokens at less than half the
+// few-row kernel's rate.  Measured with 16 sequences of 8192 tokens and 4 cache heads (us, few-row
+// kernel / chunk kernel):
+//              16 rows      32 rows      48 rows     64 rows    128 rows
+//   BF16  64   44 / 64      62 / 64      79 / 64     95 / 64    156 / 66
+//   BF16 128   68 / 83     107 / 83     144 / 85    175 / 83    304 / 83
+//   BF16 256  100 / 151    174 / 151    249 / 152   325 / 151   598 / 152
+//   MXFP8 64   31 / 79      44 / 79      58 / 79     70 / 79    126 / 81
+//   MXFP8 128  48 / 148     64 / 148     93 / 148   109 / 148   197 / 148
+//   MXFP8 256  79 / 189    126 / 189    173 / 189   216 / 189   400 / 189
+//   MXFP4 64   31 / 74      44 / 74      58 / 74     70 / 74    128 / 74
+//   MXFP4 128  42 / 97      64 / 98      87 / 99    107 / 98    197 / 99
+//   MXFP4 256  70 / 168    115 / 171    162 / 171   206 / 169   390 / 171
+// which is the first rule.  The second: where there is little to do in all, the shorter start
+// decides whatever the rows (one sequence of 4096 tokens, 64 rows: BF16 19 / 36, MXFP8 23 / 54,
+// MXFP4 21 / 50 with heads of 128; BF16 25 / 46 with heads of 256).  The lengths are not known
+// here; what the tables and the window allow bounds them.
+bool takes_few(const AttnParams& p, int type, int D, long long rows) {
+  if (rows <= (type == FT_KV_BF16 ? 16 : D == 256 ? 48 : 64)) return true;
+  const long long tokens = (long long)p.n_tokens * p.group;
+  const long long blocks = std::min(p.n_seqs * ((rows + 31) / 32), tokens / 32 + p.n_seqs);  // of 32 rows
+  long long seen = (long long)p.table_stride * p.page_size;
+  if (p.window > 0) seen = std::min(seen, p.window + rows / p.group);
+  const double work = (double)blocks * p.n_kv_heads * seen * D;  // the two meet at 0.13 to 0.5 of 2^27
+  return work <= (type == FT_KV_BF16 ? 1 << 24 : 1 << 25);
+}
 
 ft_status check_heads(const char* name, int n_heads, int n_kv_heads, int head_dim) {
   if (n_kv_heads < 1 || n_kv_heads > 1024 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128)
@@ -134,9 +165,11 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, int, cudaStream_t);
   static const Kernel kernels[2][3] = {{kv::attn_rows_bf16, kv::attn_rows_mxfp8, kv::attn_rows_mxfp4},
                                        {kv::attn_chunk_bf16, kv::attn_chunk_mxfp8, kv::attn_chunk_mxfp4}};
-  const long long rows = (long long)a->max_new * p.group;  // of one cache head of a sequence, at most
+  const long long rows = (long long)std::min(a->max_new, a->n_tokens) * p.group;  // of one cache head of a sequence, at most
   cudaError_t e = cudaSuccess;
-  if (c->kv_type != FT_KV_BF16 && rows >= kv::kStageRows && a->workspace_bytes >= least + kv::kStageHead + kv::kStageBytes) {
+  if (kv::takes_few(p, c->kv_type, c->head_dim, rows)) {
+    e = kernels[0][c->kv_type](p, c->head_dim, (int)(rows < 33 ? rows : 33), n_sm, s);
+  } else if (c->kv_type != FT_KV_BF16 && rows >= kv::kStageRows && a->workspace_bytes >= least + kv::kStageHead + kv::kStageBytes) {
     // many rows over a quantised cache: its pages are decoded once
     uint8_t* at = static_cast<uint8_t*>(a->workspace) + least;
     const size_t page = (size_t)c->n_kv_heads * c->page_size * c->head_dim * 2;
@@ -168,7 +201,7 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
       e = kernels[1][FT_KV_BF16](p, c->head_dim, 33, n_sm, s);
     }
   } else {
-    e = kernels[rows > 32][c->kv_type](p, c->head_dim, (int)(rows < 33 ? rows : 33), n_sm, s);
+    e = kernels[1][c->kv_type](p, c->head_dim, 33, n_sm, s);
   }
   return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
