@@ -1,5 +1,6 @@
 // ft_attn: argument checks, workspace and the choice of the kernel.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "ft_kv_internal.cuh"
@@ -47,9 +48,15 @@ constexpr size_t kStageBytes = (size_t)512 << 20;
 // 240 and 195; 2048: 406 and 296.  MXFP4 512 rows 130 and 150; 1024: 179 and 185; 2048: 301 and 288.
 constexpr int kStageRows = 1024;
 
+// Tokens of the cache that a sequence's new ones may see, at most (its length is not known here).
+long long may_see(const AttnParams& p, long long rows) {
+  const long long cap = (long long)p.table_stride * p.page_size;
+  return p.window > 0 ? std::min(cap, p.window + rows / p.group) : cap;
+}
+
 // Whether the few-row kernel takes a batch (rows: of one cache head of a sequence, at most).  It
 // re-reads the cache for every 16 or 32 rows; the chunk kernel does so for every 256, but takes
-// 12 us longer to start and to end, and decodes a quantised cache's tokens at less than half the
+// 12 us longer to start and to end, and decodes a quantised cache's tokens at about half the
 // few-row kernel's rate.  Measured with 16 sequences of 8192 tokens and 4 cache heads (us, few-row
 // kernel / chunk kernel):
 //              16 rows      32 rows      48 rows     64 rows    128 rows
@@ -57,7 +64,7 @@ constexpr int kStageRows = 1024;
 //   BF16 128   68 / 83     107 / 83     144 / 85    175 / 83    304 / 83
 //   BF16 256  100 / 151    174 / 151    249 / 152   325 / 151   598 / 152
 //   MXFP8 64   31 / 79      44 / 79      58 / 79     70 / 79    126 / 81
-//   MXFP8 128  48 / 148     64 / 148     93 / 148   109 / 148   197 / 148
+//   MXFP8 128  48 / 113     64 / 113     93 / 113   109 / 113   197 / 113
 //   MXFP8 256  79 / 189    126 / 189    173 / 189   216 / 189   400 / 189
 //   MXFP4 64   31 / 74      44 / 74      58 / 74     70 / 74    128 / 74
 //   MXFP4 128  42 / 97      64 / 98      87 / 99    107 / 98    197 / 99
@@ -70,10 +77,22 @@ bool takes_few(const AttnParams& p, int type, int D, long long rows) {
   if (rows <= (type == FT_KV_BF16 ? 16 : D == 256 ? 48 : 64)) return true;
   const long long tokens = (long long)p.n_tokens * p.group;
   const long long blocks = std::min(p.n_seqs * ((rows + 31) / 32), tokens / 32 + p.n_seqs);  // of 32 rows
-  long long seen = (long long)p.table_stride * p.page_size;
-  if (p.window > 0) seen = std::min(seen, p.window + rows / p.group);
-  const double work = (double)blocks * p.n_kv_heads * seen * D;  // the two meet at 0.13 to 0.5 of 2^27
+  const double work = (double)blocks * p.n_kv_heads * may_see(p, rows) * D;  // the two meet at 0.13 to 0.5 of 2^27
   return work <= (type == FT_KV_BF16 ? 1 << 24 : 1 << 25);
+}
+
+// Whether a batch's sequences of few rows (single tokens, mostly) get a launch of the few-row
+// kernel of their own, before the one for the others: sequences of different numbers of new tokens,
+// and much to read.  Measured (us, one launch / two), one chunk besides single tokens that each see
+// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 142 / 99, 4 x 128 117 / 120,
+// 2 x 256 132 / 145; 31 and a chunk of 512 over 2048: MXFP8 350 / 121, 300 / 133, 313 / 149, MXFP4
+// 312 / 122, 270 / 122, 288 / 141, BF16 203 / 154, 158 / 159, 167 / 173; 63 and a chunk of 1024 over
+// 8192: MXFP8 590 / 235, 477 / 278, 587 / 290, BF16 449 / 289, 349 / 323, 359 / 316.  With little to
+// read the second launch costs more than it saves (7 that see 1000 and a chunk of 1024: 57 / 86).
+constexpr int kFewRows = 16;
+bool splits(const AttnParams& p, int type, int D, long long rows, int max_new) {
+  return p.n_tokens < (long long)p.n_seqs * max_new &&
+         (double)p.n_seqs * p.n_kv_heads * may_see(p, rows) * D >= (type == FT_KV_BF16 ? 1 << 28 : 1 << 26);
 }
 
 ft_status check_heads(const char* name, int n_heads, int n_kv_heads, int head_dim) {
@@ -160,6 +179,8 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   p.lse = a->lse;
   p.counters = static_cast<uint32_t*>(a->workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kv::kCounterBytes + 256);
+  p.rows_min = 0;
+  p.rows_max = INT_MAX;
   p.error_word = a->error_word_out ? a->error_word_out : p.counters + kv::kMaxCtas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using Kernel = cudaError_t (*)(const kv::AttnParams&, int, int, int, cudaStream_t);
@@ -169,7 +190,16 @@ extern "C" ft_status ft_attn(const ft_kv_cache* c, const ft_attn_args* a, void* 
   cudaError_t e = cudaSuccess;
   if (kv::takes_few(p, c->kv_type, c->head_dim, rows)) {
     e = kernels[0][c->kv_type](p, c->head_dim, (int)(rows < 33 ? rows : 33), n_sm, s);
-  } else if (c->kv_type != FT_KV_BF16 && rows >= kv::kStageRows && a->workspace_bytes >= least + kv::kStageHead + kv::kStageBytes) {
+    return e == cudaSuccess ? FT_OK : kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+  }
+  if (kv::splits(p, c->kv_type, c->head_dim, rows, a->max_new)) {
+    p.rows_max = kv::kFewRows;
+    e = kernels[0][c->kv_type](p, c->head_dim, kv::kFewRows, n_sm, s);
+    if (e != cudaSuccess) return kv_fail(FT_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    p.rows_min = kv::kFewRows + 1;
+    p.rows_max = INT_MAX;
+  }
+  if (c->kv_type != FT_KV_BF16 && rows >= kv::kStageRows && a->workspace_bytes >= least + kv::kStageHead + kv::kStageBytes) {
     // many rows over a quantised cache: its pages are decoded once
     uint8_t* at = static_cast<uint8_t*>(a->workspace) + least;
     const size_t page = (size_t)c->n_kv_heads * c->page_size * c->head_dim * 2;

@@ -56,13 +56,21 @@ struct Cfg {
   static constexpr int walks = q ? 8 * 96 : 0;             // where the loaders' walks wait
   static constexpr int smem = 1024 + qbytes + 2 * stages * stage + out_bytes + 512 + walks;
   // Registers of the softmax, MMA and loader warps out of those that the block starts with:
-  // BF16, two tiles (168 x 384 = 64512): 208 x 256 + 88 x 128 = 64512;
-  // quantised, two tiles (96 x 640 = 61440): 136 x 256 + 80 x 128 + 64 x 256 = 61440;
+  // BF16, two tiles (168 x 384 = 64512): 216 x 256 + 72 x 128 = 64512;
+  // quantised, two tiles (96 x 640 = 61440): 136 x 256 + 48 x 128 + 80 x 256 = 61440
+  // (64 for the loaders leaves their loads in flight no room: MXFP8, heads of 128, 512 rows over 16 x 8192
+  // tokens 265 us, with 72 203, with 80 197);
   // quantised, one tile (128 x 512 = 65536): 192 x 128 + 64 x 128 + 128 x 256 = 65536.
   static constexpr bool split = q || tiles == 2;
-  static constexpr int soft_regs = !q ? 208 : tiles == 2 ? 136 : 192;
-  static constexpr int mma_regs = !q ? 88 : tiles == 2 ? 80 : 64;
-  static constexpr int load_regs = tiles == 2 ? 64 : 128;
+  static constexpr int soft_regs = !q ? 216 : tiles == 2 ? 136 : 192;
+  static constexpr int mma_regs = !q ? 72 : tiles == 2 ? 48 : 64;
+  static constexpr int load_regs = tiles == 2 ? 80 : 128;
+  // what the block starts with; the softmax warps raise their share, the others give some up (a
+  // warp that asks to give up and names more than it has is an illegal instruction)
+  static constexpr int launch_regs = 65536 / threads / 8 * 8 < 256 ? 65536 / threads / 8 * 8 : 255;
+  static_assert(!split || (soft_regs >= launch_regs && mma_regs <= launch_regs && (!q || load_regs <= launch_regs) &&
+                           32 * (soft_warps * soft_regs + 4 * mma_regs + (q ? 8 * load_regs : 0)) <= launch_regs * threads),
+                "shares of the registers");
   static constexpr int batch = !q && tiles == 2 ? 128 : 64;  // score columns that a softmax thread holds
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
   static constexpr int o_col = 256;  // TMEM: S (and P) at 0 and 128, O behind

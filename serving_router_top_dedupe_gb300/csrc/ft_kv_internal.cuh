@@ -75,6 +75,7 @@ struct AttnParams {
   uint32_t* counters;  // [kMaxCtas], zero between calls
   float* partials;
   uint32_t* error_word;  // never NULL
+  int rows_min, rows_max;  // sequences of fewer or more rows of a head are another launch's
   // A copy of the pages that the batch sees, decoded to BF16 (stage_pages): k, v and n_pages are
   // the copy's, and page j of sequence s is its page staged[s] + j.  NULL: the cache itself.
   const int32_t* staged;
@@ -124,6 +125,7 @@ __device__ __forceinline__ void seq_range(const AttnParams& p, int s, int& q0, i
   q0 = min(max(a, 0), p.n_tokens);
   n = max(min(max(b, 0), p.n_tokens) - q0, 0);
   len = min(max(l, 0), cap);
+  if (n * p.group < p.rows_min || n * p.group > p.rows_max) n = 0;
   bad = a != q0 || b < a || b > p.n_tokens || l != len;
 }
 

@@ -232,3 +232,16 @@ def test_pages_beyond_four_gigabytes(F, kind, new):
         assert torch.equal(a, b)
     if kind == 0:
         assert torch.equal(got[0][0], k) and torch.equal(got[0][1], v)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(24, 8, 64), (32, 4, 128), (16, 2, 256)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_batches_of_single_tokens_and_chunks(F, kind, heads, kv_heads, dim, window):
+    """Sequences of few and of many rows side by side, with tables that name enough to read for a launch each."""
+    new, lens = [1, 90, 2, 1, 0, 130, 1, 3], [1000, 90, 2, 777, 50, 400, 1, 0]
+    b = Batch(F, kind, heads, kv_heads, dim, 64, new=new, lens=lens, window=window, extra_rows=3)
+    widen(b, 1 << 14, 130).check()
+    first = b.out.clone()
+    b.check()
+    assert torch.equal(first, b.out)
