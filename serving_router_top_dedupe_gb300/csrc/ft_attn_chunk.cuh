@@ -104,6 +104,17 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Whether a phase has passed, without waiting for it.
+__device__ __forceinline__ bool passed(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: 8-row atoms of 1024 bytes (stride byte
 // offset); lead: bytes from one 64-column panel to the next, for the operand whose columns
 // run along the 128-byte rows (V), unused by the other (Q, K).  desc_lo is the low word, to
@@ -734,22 +745,26 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
           ph ^= 1u;
         }
       };
-      // scores of row tile x into S buffer u, from the K stage at kst
-      auto scores = [&](int x, int u) {
+      // scores of row tile x into S buffer u, from the K stage at kst.  mid: what the thread does
+      // while the last two MMAs are still to be issued, and the ones before keep the tensor core.
+      auto scores = [&](int x, int u, auto mid) {
         const uint32_t a = desc_lo(q_addr + x * C::stage, 0), b = desc_lo(ring_addr + kst * C::stage, 0);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
+          if (k == D / 16 - 2) mid();
           const uint32_t off = ((k >> 2) * PANEL + 32 * (k & 3)) >> 4;
           mma_ss(tmem + 128 * u, desc(a + off), desc(b + off), idesc(128, KT, 0), k != 0);
         }
         commit(bar(s_full + u));
       };
-      auto product = [&](int x, int u, bool first, bool last) {
+      auto product = [&](int x, int u, bool first, bool last, auto mid) {
         const uint32_t b = desc_lo(ring_addr + (NS + vst) * C::stage, PANEL);
 #pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
+        for (int k = 0; k < KT / 16; ++k) {
+          if (k == KT / 16 - 2) mid();
           mma_ts(tmem + C::o_col + x * D, tmem + 128 * u + 8 * k, desc(b + (2048 >> 4) * k), idesc(128, D, 1),
                  !(first && k == 0));
+        }
         if (T == 1 || last) commit(bar(o_full + x));
       };
       auto wait_q = [&](int x) {
@@ -767,8 +782,10 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         if (C::pair) commit_pair(bar(b));
         else commit(bar(b));
       };
-      // The issuing thread must not keep the tensor core waiting: what changes from item to item
-      // is worked out between items.
+      auto nothing = [] {};
+      // The issuing thread must not keep the tensor core waiting, whose queue holds about three
+      // MMAs: what changes from item to item is worked out between items, and waits and releases
+      // that need not stand between two batches of MMAs are done inside a batch.
       uint32_t u = 0;  // S buffer of the step (one row tile)
       bool ok = true;
       while (ok && wk.more()) {
@@ -777,41 +794,50 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         // the first scores of the item
         if (!(ok = wait(full + kst, kph) && wait_q(0))) break;
         tc_after();
-        scores(0, T == 2 ? 0 : u);
+        scores(0, T == 2 ? 0 : u, nothing);
         if (two) {
           if (!(ok = wait_q(1))) break;
-          scores(1, 1);
+          scores(1, 1, nothing);
         }
         release(empty + kst);
         advance(kst, kph);
+        bool p_there = false;  // of the second row tile, seen ahead of time
         for (int j = 0; j < n; ++j) {
           const bool more = j + 1 < n;
           if (T == 2) {  // product and next scores of one row tile, then of the other
-            // What is between two batches of MMAs is kept short: the tensor core's queue holds three.
             if (!(ok = wait(full + NS + vst, vph) && (!more || wait(full + kst, kph)) && wait_p(0))) break;
-            product(0, 0, j == 0, !more);
-            if (more) scores(0, 0);
+            product(0, 0, j == 0, !more, nothing);
+            auto let_v_go = [&] {
+              release(empty + NS + vst);
+              advance(vst, vph);
+            };
             if (two) {
-              if (!(ok = wait_p(1))) break;
-              product(1, 1, j == 0, !more);
+              if (more) scores(0, 0, [&] { p_there = passed(bar(p_full + 1), (p_ph >> 1) & 1); });
+              if (more && p_there) {
+                p_ph ^= 2u;
+                tc_after();
+              } else if (!(ok = wait_p(1))) {
+                break;
+              }
+              product(1, 1, j == 0, !more, nothing);
             }
-            release(empty + NS + vst);
-            advance(vst, vph);
             if (more) {
-              if (two) scores(1, 1);
+              scores(two, two, let_v_go);
               release(empty + kst);
               advance(kst, kph);
+            } else {
+              let_v_go();
             }
           } else {  // the next scores are formed during the softmax
             if (more) {
               if (!(ok = wait(full + kst, kph))) break;
               tc_after();
-              scores(0, u ^ 1);
+              scores(0, u ^ 1, nothing);
               release(empty + kst);
               advance(kst, kph);
             }
             if (!(ok = wait(full + NS + vst, vph) && wait_p(u))) break;
-            product(0, u, j == 0, !more);
+            product(0, u, j == 0, !more, nothing);
             release(empty + NS + vst);
             advance(vst, vph);
             u ^= 1;
