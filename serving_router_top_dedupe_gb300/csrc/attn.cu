@@ -43,9 +43,9 @@ constexpr size_t kStageHead = kMaxSeqs * 4 + 256;
 constexpr size_t kStageBytes = (size_t)512 << 20;
 
 // From this many rows of a head on, a quantised cache's pages are decoded once into a BF16 copy;
-// below it each block of 256 rows decodes what it reads.  Both sides measured (us, 16 query heads
-// over 4 cache heads of 128, 65536 cached tokens): MXFP8 512 rows 165 direct, 158 copied; 1024:
-// 240 and 195; 2048: 406 and 296.  MXFP4 512 rows 130 and 150; 1024: 179 and 185; 2048: 301 and 288.
+// below it each block of 256 rows decodes what it reads.  Both sides measured (us, decoded where
+// it is read / copied; 16 query heads over 4 cache heads of 128, 16 sequences of 4096 tokens):
+// MXFP8 512 rows 119 / 136, 1024 197 / 183, 2048 347 / 285; MXFP4 107 / 126, 179 / 175, 314 / 275.
 constexpr int kStageRows = 1024;
 
 // Tokens of the cache that a sequence's new ones may see, at most (its length is not known here).
@@ -60,15 +60,15 @@ long long may_see(const AttnParams& p, long long rows) {
 // few-row kernel's rate.  Measured with 16 sequences of 8192 tokens and 4 cache heads (us, few-row
 // kernel / chunk kernel):
 //              16 rows      32 rows      48 rows     64 rows    128 rows
-//   BF16  64   44 / 64      62 / 64      79 / 64     95 / 64    156 / 66
-//   BF16 128   68 / 83     107 / 83     144 / 85    175 / 83    304 / 83
-//   BF16 256  100 / 151    174 / 151    249 / 152   325 / 151   598 / 152
-//   MXFP8 64   31 / 79      44 / 79      58 / 79     70 / 79    126 / 81
-//   MXFP8 128  48 / 113     64 / 113     93 / 113   109 / 113   197 / 113
-//   MXFP8 256  79 / 189    126 / 189    173 / 189   216 / 189   400 / 189
-//   MXFP4 64   31 / 74      44 / 74      58 / 74     70 / 74    128 / 74
-//   MXFP4 128  42 / 97      64 / 98      87 / 99    107 / 98    197 / 99
-//   MXFP4 256  70 / 168    115 / 171    162 / 171   206 / 169   390 / 171
+//   BF16  64   44 / 62      62 / 62      79 / 62     97 / 62    156 / 62
+//   BF16 128   68 / 83     107 / 83     144 / 83    181 / 83    316 / 85
+//   BF16 256  100 / 152    174 / 152    249 / 152   329 / 152   615 / 152
+//   MXFP8 64   31 / 76      44 / 76      58 / 76     70 / 76    126 / 76
+//   MXFP8 128  48 / 115     64 / 115     93 / 115   109 / 115   197 / 115
+//   MXFP8 256  79 / 197    126 / 197    173 / 197   216 / 197   400 / 199
+//   MXFP4 64   31 / 73      44 / 73      58 / 73     70 / 74    128 / 72
+//   MXFP4 128  42 / 103     64 / 103     87 / 103   107 / 103   197 / 105
+//   MXFP4 256  70 / 179    115 / 179    162 / 179   205 / 179   390 / 179
 // which is the first rule.  The second: where there is little to do in all, the shorter start
 // decides whatever the rows (one sequence of 4096 tokens, 64 rows: BF16 19 / 36, MXFP8 23 / 54,
 // MXFP4 21 / 50 with heads of 128; BF16 25 / 46 with heads of 256).  The lengths are not known
@@ -84,10 +84,10 @@ bool takes_few(const AttnParams& p, int type, int D, long long rows) {
 // Whether a batch's sequences of few rows (single tokens, mostly) get a launch of the few-row
 // kernel of their own, before the one for the others: sequences of different numbers of new tokens,
 // and much to read.  Measured (us, one launch / two), one chunk besides single tokens that each see
-// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 142 / 99, 4 x 128 117 / 120,
-// 2 x 256 132 / 145; 31 and a chunk of 512 over 2048: MXFP8 350 / 121, 300 / 133, 313 / 149, MXFP4
-// 312 / 122, 270 / 122, 288 / 141, BF16 203 / 154, 158 / 159, 167 / 173; 63 and a chunk of 1024 over
-// 8192: MXFP8 590 / 235, 477 / 278, 587 / 290, BF16 449 / 289, 349 / 323, 359 / 316.  With little to
+// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 142 / 97, 4 x 128 117 / 120,
+// 2 x 256 132 / 144; 31 and a chunk of 512 over 2048: MXFP8 350 / 121, 300 / 134, 313 / 148, MXFP4
+// 312 / 121, 270 / 121, 288 / 140, BF16 191 / 154, 152 / 159, 165 / 173; 63 and a chunk of 1024 over
+// 8192: MXFP8 590 / 229, 477 / 276, 587 / 288, BF16 449 / 281, 349 / 318, 359 / 318.  With little to
 // read the second launch costs more than it saves (7 that see 1000 and a chunk of 1024: 57 / 86).
 constexpr int kFewRows = 16;
 bool splits(const AttnParams& p, int type, int D, long long rows, int max_new) {
