@@ -93,7 +93,7 @@ typedef struct {
   int n_seqs;               /* sequences, at most 1024 */
   int max_new;              /* new tokens of one sequence, at most: chooses the kernel, and any value >= 1
                                gives the same results within rounding */
-  int table_stride;         /* pages of one row of page_table */
+  int table_stride;         /* pages of one row of page_table; times page_size at most 2^30 */
   int causal;               /* 1: a token sees no later one; 0: every token sees the whole length */
   int window;               /* 0, or how many tokens up to its own position a token sees */
   float scale;              /* of the scores; finite */
@@ -110,16 +110,23 @@ typedef struct {
   uint32_t* error_word_out; /* optional dev uint32, into which FT_DEVERR_* bits are OR-ed */
 } ft_attn_args;
 
-/* Bytes of workspace that ft_attn needs on the current device, for any batch.  The caller sets
- * the workspace to zero once, before its first use; every call leaves it ready for the next.
- * Calls that may overlap on the GPU need workspaces of their own.
+/* Bytes of workspace that ft_attn uses on the current device, for any batch.  The caller sets
+ * the workspace to zero once, before its first use; every call leaves it ready for the next
+ * (after FT_DEVERR_TIMEOUT, a wait inside a kernel that ran out, it is to be set to zero again, and
+ * the call's outputs are not to be used).  Calls that may overlap on the GPU need workspaces of
+ * their own.  The last FT_ATTN_COPY_BYTES hold decoded pages of a quantised cache under chunks of
+ * many rows; a workspace without them is taken too, and the pages are then decoded where they are
+ * read, for every 256 rows again.
  * Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+#define FT_ATTN_COPY_BYTES (((size_t)512 << 20) + 4352)
 ft_status ft_attn_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes_out);
 
 /* Attention of a batch's new tokens over the paged cache: single tokens (decode), a few
  * (checking drafted tokens) or whole chunks (prefill), mixed as they come.  Scores, softmax
  * statistics and sums are FP32; probabilities are rounded to BF16 for their product with the
- * values.  The same inputs give the same bits.  Rows of q that no sequence names are left
+ * values (to FP16, with the values' scale, for few rows over a quantised cache).  Which kernels run
+ * follows from n_tokens, n_seqs, max_new, window and table_stride: a table much wider than the
+ * lengths makes small batches slower.  The same arguments and inputs give the same bits.  Rows of q that no sequence names are left
  * unwritten in out and lse.  A length beyond table_stride pages, offsets outside
  * [0, n_tokens] or out of order, and page ids beyond the cache set FT_DEVERR_BAD_INDEX: the
  * length or offset is limited to its range, a bad page's tokens count as rows of zeros.

@@ -40,7 +40,8 @@ size_t partial_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * (D == 256 ? 12
 // each sequence's pages begin in it, whether it had room, and the copy.
 size_t workspace_least(int n_sm, int D) { return kCounterBytes + 256 + partial_bytes(n_sm, D); }
 constexpr size_t kStageHead = kMaxSeqs * 4 + 256;
-constexpr size_t kStageBytes = (size_t)512 << 20;
+constexpr size_t kStageBytes = FT_ATTN_COPY_BYTES - kStageHead;
+static_assert(kStageHead == 4352, "the copy's part of the workspace");
 
 // From this many rows of a head on, a quantised cache's pages are decoded once into a BF16 copy;
 // below it each block of 256 rows decodes what it reads.  Both sides measured (us, decoded where

@@ -1,6 +1,10 @@
 // Attention of few rows over the paged cache: single tokens, a few drafted tokens, and
 // (block by block) any number of rows.
 //
+// Every part of an item keeps, for each row, m (a bound of the scores so far, in units of log 2),
+// l = sum 2^(s_j - m) and o = sum 2^(s_j - m) v_j in FP32; parts with other bounds are added
+// after multiplying with 2^(m - m').  out = o / l, lse = log 2 * (m + log2 l).
+//
 // A block is 16 or 32 rows of one cache head (the query heads of the group, times new tokens):
 // one or two row tiles of mma.sync.  Each cached byte is used by these rows only, so reading the
 // cache bounds this kernel, and next to that the decoding of quantised caches:
@@ -21,6 +25,16 @@
 //    which become the operands of 2 (4) column tiles.
 // The running maximum moves only when a score passes it by 2^8 or more, so the accumulators
 // are rarely rescaled.
+//
+// Roundings: probabilities to BF16 for their product with BF16 values, to FP16 (after the values'
+// scale) with quantised ones: one rounding of 2^-9 or 2^-12 of each term, what the tensor core
+// takes; everything summed is FP32.
+//
+// Measured: 64 single tokens over 16384 tokens each, 4 cache heads of 128, 8 rows of a head: BF16
+// 320 us = 6.7 TB/s, bound by memory; MXFP8 193 us = 5.7 TB/s; MXFP4 193 us = 3.0 TB/s, bound by the
+// decoding: both take the same instructions for a chunk, about 970, and issue one in 52 % of the
+// clocks; 32 rows 315 and 302 us.  One sequence of 4001 tokens: 15 us, of which a launch, the plan,
+// two tiles' latency and the join are nearly all.
 #pragma once
 
 #include "ft_attn_redo.cuh"
@@ -128,17 +142,22 @@ template <int TYPE, int D, int MT>
 struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
   static constexpr int RB = 16 * MT;  // rows of a block
-  // Tokens of a warp's step.  Quantised: twice as many independent products in a chain that
-  // is long for decoding; 256-wide heads have no registers for that.
+  // Tokens of a warp's step.  Quantised: twice as many independent products in a chain that is long
+  // for decoding (32 / 16 tokens: MXFP8 8 rows 193 / 217 us, MXFP4 193 / 215 at the size above; 32 rows
+  // 315 / 346 and 302 / 330); 256-wide heads have no registers for that, BF16 has no such chain.
   static constexpr int CHUNK = q && D <= 128 ? 32 : 16;
   static constexpr int UT = CHUNK * kWarps;          // tokens of a tile
-  static constexpr int OV = CHUNK == 32 ? 3 : 6;     // counts of an item besides its tiles
-  static constexpr float join_cost = 0.35f;          // tiles' time that a part of an item costs the join
+  // Counts of an item besides its tiles (64 ragged MXFP8 sequences: 0 91 us, 3 55, 8 62).
+  static constexpr int OV = CHUNK == 32 ? 3 : 6;
+  // Tiles' time that a part of an item costs the join (the same 55 us, with 2.0 68; one sequence
+  // of 4001 tokens 15 and 20 us).
+  static constexpr float join_cost = 0.35f;
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
   static constexpr int scales = q ? 2 * CHUNK * (D / 32) * 4 : 0;  // a warp's chunk of scales in FP32
-  static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;  // per SM
+  // per SM, as registers allow (MXFP8, 4 CTAs of 128 registers: 232 us in place of 193)
+  static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;
   static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 66 * 1024;
   static constexpr int fit = room / (kWarps * stage);
   static constexpr int stages = fit < 8 ? fit : 8;
@@ -804,7 +823,9 @@ cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
   return launch_k(attn_rows_kernel<TYPE, D, MT>, dim3(grid), dim3(kThreads), C::smem, s, true, p);
 }
 
-// rows: of one cache head of a sequence, at most.
+// rows: of one cache head of a sequence, at most.  Up to 16 rows take one row tile (the second
+// one's products would be for nothing: 193 / 315 us above), more take two, for which a chunk is
+// decoded once; 256-wide heads have registers for one.
 template <int TYPE>
 cudaError_t launch_type(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s) {
   if (D == 64) return rows <= 16 ? launch<TYPE, 64, 1>(p, n_sm, s) : launch<TYPE, 64, 2>(p, n_sm, s);
