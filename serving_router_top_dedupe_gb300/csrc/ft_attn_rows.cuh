@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       float ve = 0.f;
       if constexpr (C::q) {
         // The chunk's scale codes as FP32 powers of two, zero for tokens that are left out; and
-        // log2 of the largest one of the values, 13 at most.
+        // log2 of the largest one of the values, 13 at most, and no less than the formats' smallest:
+        // where no token has a scale that is a number (pages that are not there, values that are all
+        // NaN), 2^ev and its inverse still have to be numbers that FP32 holds.
         const uint8_t* codes = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
         // Lane l takes the codes of token l % CHUNK: with 16 tokens of K or of V, with 32 of both.
         constexpr int SETS = CHUNK / 16;
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        ve = fminf((float)top - 127.f, 13.f);
+        ve = fminf(fmaxf((float)top - 127.f, -100.f), 13.f);
         __syncwarp();
       }
       // of a block: this thread's tokens 2c, 2c+1 of column tile nt
