@@ -123,8 +123,9 @@ ft_status ft_attn_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* b
 
 /* Attention of a batch's new tokens over the paged cache: single tokens (decode), a few
  * (checking drafted tokens) or whole chunks (prefill), mixed as they come.  Scores, softmax
- * statistics and sums are FP32; probabilities are rounded to BF16 for their product with the
- * values (to FP16, with the values' scale, for few rows over a quantised cache).  Which kernels run
+ * statistics and sums are FP32; probabilities (times the scale of quantised values) are rounded to
+ * BF16 for their product with the values, each term relative to itself.  Few rows over a quantised
+ * cache take query elements below 2^-28 of their row's largest to within 2^-39 of it.  Which kernels run
  * follows from n_tokens, n_seqs, max_new, window and table_stride: a table much wider than the
  * lengths makes small batches slower.  The same arguments and inputs give the same bits.  Rows of q that no sequence names are left
  * unwritten in out and lse.  A length beyond table_stride pages, offsets outside

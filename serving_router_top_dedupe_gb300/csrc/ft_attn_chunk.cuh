@@ -39,6 +39,8 @@ namespace ft {
 namespace kv {
 namespace chunk {
 
+using rows::e2m1_bits;
+using rows::e4m3_bits;
 using rows::ex2;
 using rows::pack;
 
@@ -220,16 +222,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Two E4M3 codes in the high bytes of both halves -> the BF16 numbers they stand for, times 2^-120.
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) { return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u); }
-// Nibble I of both halves -> the BF16 numbers their E2M1 codes stand for, times 2^-126.
-template <int I>
-__device__ __forceinline__ uint32_t e2m1_bits(uint32_t w) {
-  const uint32_t mag = I == 0 ? w << 6 : I == 1 ? w << 2 : I == 2 ? w >> 2 : w >> 6;
-  const uint32_t sgn = w << (12 - 4 * I);
-  return (mag & 0x01C001C0u) | (sgn & 0x80008000u);
-}
-
 // Scale code -> a pair of BF16 multipliers: 2^e (NaN for code 255) times what the codes' bits lack.
 template <int TYPE>
 __device__ __forceinline__ uint32_t multiplier(uint32_t code) {
@@ -256,8 +248,8 @@ __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
   if (TYPE == FT_KV_MXFP8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o[2 * i] = mul2(e4m3_bits(__byte_perm(in[i], 0, 0x1404)), m);
-      o[2 * i + 1] = mul2(e4m3_bits(__byte_perm(in[i], 0, 0x3424)), m);
+      o[2 * i] = mul2(e4m3_bits<true>(__byte_perm(in[i], 0, 0x1404)), m);
+      o[2 * i + 1] = mul2(e4m3_bits<true>(__byte_perm(in[i], 0, 0x3424)), m);
     }
   } else {
 #pragma unroll

@@ -14,11 +14,15 @@
 //    end of the CTA's part of the item;
 //  - rows lie in shared memory with their 16-byte pieces permuted by the row, so ldmatrix reads
 //    keys and (transposed) values without bank conflicts;
-//  - MXFP8 and MXFP4 codes go from ldmatrix to FP16 operands in registers, one conversion for
-//    two elements: FP16 holds every E4M3 and E2M1 number.  Their scales stay outside: a 1x32
-//    block of keys is a product of its own, added to the scores times its scale in FP32; a
-//    block of values takes probabilities times its scale.  The queries become FP16 times a
-//    power of two that brings a row's largest to 2^14 (exact for elements down to 2^-28 of it).
+//  - MXFP8 and MXFP4 codes go from ldmatrix to operands in registers.  Their scales stay outside.
+//    Keys become FP16 (one conversion for two elements; FP16 holds every E4M3 and E2M1 number),
+//    and a 1x32 block of them is a product of its own, added to the scores times its scale in
+//    FP32.  The queries become FP16 times a power of two that brings a row's largest to 2^14 (exact
+//    for elements down to 2^-28 of it; smaller ones are off by 2^-39 of the largest at most).
+//    Values become BF16 (their codes' bits in BF16's places: the numbers times 2^-120 or 2^-126),
+//    and probabilities take their scale and most of what the bits lack before they become BF16
+//    too: FP32's exponents, so a term is rounded relative to itself, whatever the scales of other
+//    tokens and blocks, seen or not, and no exponent is kept beside the running maximum.
 //  - The order of the reduction is free, and so is the order of the value columns: keys are
 //    taken in the order in which a 32-bit word holds their codes, with the queries arranged to
 //    match, and a transposed 16-bit unit holds 2 (4) neighbouring value columns of a token,
@@ -26,9 +30,9 @@
 // The running maximum moves only when a score passes it by 2^8 or more, so the accumulators
 // are rarely rescaled.
 //
-// Roundings: probabilities to BF16 for their product with BF16 values, to FP16 (after the values'
-// scale) with quantised ones: one rounding of 2^-9 or 2^-12 of each term, what the tensor core
-// takes; everything summed is FP32.
+// Roundings: probabilities (times the scale of quantised values) to BF16 for their product with the
+// values: one rounding of half a unit in the last of 8 bits of each term, what the tensor core takes;
+// everything summed is FP32.
 //
 // Measured: 64 single tokens over 16384 tokens each, 4 cache heads of 128, 8 rows of a head: BF16
 // 320 us = 6.7 TB/s, bound by memory; MXFP8 193 us = 5.7 TB/s; MXFP4 193 us = 3.0 TB/s, bound by the
@@ -125,6 +129,19 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& h
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// E4M3 codes in the low (HIGH: high) bytes of both halves -> the BF16 numbers they stand for, times
+// 2^-120.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t w) {
+  return ((HIGH ? w >> 4 : w << 4) & 0x07F007F0u) | ((HIGH ? w : w << 8) & 0x80008000u);
+}
+// Nibble I of both halves -> the BF16 numbers their E2M1 codes stand for, times 2^-126.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_bits(uint32_t w) {
+  const uint32_t mag = I == 0 ? w << 6 : I == 1 ? w << 2 : I == 2 ? w >> 2 : w >> 6;
+  const uint32_t sgn = w << (12 - 4 * I);
+  return (mag & 0x01C001C0u) | (sgn & 0x80008000u);
+}
 // Byte i of a word: two E2M1 codes -> an FP16 pair.
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t* r) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -138,6 +155,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 template <int TYPE, int D, int MT>
 struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
@@ -171,6 +190,11 @@ struct Cfg {
   static constexpr int body = max1 > (int)sizeof(PlanSmem) ? max1 : (int)sizeof(PlanSmem);
   static constexpr int smem = qfrag + head + body + kWarps * scales;
   static constexpr size_t slot_floats = (size_t)RB * (D + 2);
+  // The values' scales are staged times 2^lack, and sums are taken back by 2^taken once at the end:
+  // together 2^120 or 2^126, which the values' bits lack.  A probability (2^8 at most) times the
+  // largest scale (2^7 or 2^13) and 2^lack stays below 2^126.
+  static constexpr int lack = TYPE == FT_KV_MXFP8 ? 108 : TYPE == FT_KV_MXFP4 ? 104 : 0;
+  static constexpr int taken = TYPE == FT_KV_MXFP8 ? 12 : TYPE == FT_KV_MXFP4 ? 22 : 0;
   static constexpr bool q_regs = D <= 128 && MT == 1 && !q;  // the queries' operands stay in registers
 };
 
@@ -380,9 +404,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
     };
     float o[MT][NT][4];
     float m[MT][2], l[MT][2];
-    // Quantised values: o is relative to 2^(m + ev), l to 2^m: ev follows the largest scale of
-    // the values, so that probabilities times scales stay below 2^14 in FP16.
-    float ev = C::q ? -1000.f : 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -402,18 +423,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       if (!wanted(k)) continue;
       const int t = tok0 + k * UT;
       const uint32_t st = ring + (uint32_t)(k % S) * C::stage;
-      float ve = 0.f;
       if constexpr (C::q) {
-        // The chunk's scale codes as FP32 powers of two, zero for tokens that are left out; and
-        // log2 of the largest one of the values, 13 at most, and no less than the formats' smallest:
-        // where no token has a scale that is a number (pages that are not there, values that are all
-        // NaN), 2^ev and its inverse still have to be numbers that FP32 holds.
+        // The chunk's scale codes as FP32 powers of two (those of the values times 2^lack), zero for
+        // tokens that are left out.
         const uint8_t* codes = ring_g + (k % S) * C::stage + 2 * C::kv_bytes;
         // Lane l takes the codes of token l % CHUNK: with 16 tokens of K or of V, with 32 of both.
         constexpr int SETS = CHUNK / 16;
         const int tok = lane % CHUNK;
         const bool in = t + tok >= cur.lo && t + tok < cur.hi;
-        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < SETS; ++i) {
           const int set = SETS == 2 ? i : lane / CHUNK;  // 0: K, 1: V
@@ -428,12 +445,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t code = (w[b >> 2] >> (8 * (b & 3))) & 0xffu;
-            sc_f[(set * NB + b) * CHUNK + tok] = in ? e8m0(code) : 0.f;
-            if (set == 1) top = max(top, in && code < 255u ? code : 0u);
+            sc_f[(set * NB + b) * CHUNK + tok] = in ? e8m0(code) * (set ? pow2(C::lack) : 1.f) : 0.f;
           }
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        ve = fminf(fmaxf((float)top - 127.f, -100.f), 13.f);
         __syncwarp();
       }
       // of a block: this thread's tokens 2c, 2c+1 of column tile nt
@@ -535,10 +549,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           move |= mx[mt][h] > m[mt][h] + kSlack;
         }
       }
-      if (C::q) move |= ve > ev + 6.f;
       if (__any_sync(0xffffffffu, move)) {
-        const float en = C::q && ve > ev + 6.f ? ve - 2.f : ev, ea = C::q ? ex2(ev - en) : 1.f;
-        ev = en;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float al[2];
@@ -551,7 +562,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
             al[h] = mn == m[mt][h] ? 1.f : ex2(m[mt][h] - mn);
             l[mt][h] *= al[h];
             m[mt][h] = mn;
-            al[h] *= ea;
           }
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -562,13 +572,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           }
         }
       }
-      const float ef = C::q ? ex2(ev) : 1.f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          // relative to 2^(m + ev); the sum is kept relative to 2^m
-          const float mu = (m[mt][h] == -INFINITY ? 0.f : m[mt][h]) + (C::q ? ev : 0.f);
+          const float mu = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
           float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < TT; ++nt)
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
               s[mt][nt][2 * h + q] = e;
               sum += e;
             }
-          l[mt][h] = fmaf(sum, ef, l[mt][h]);
+          l[mt][h] += sum;
         }
       // ------------------------------------------------------------ values
       const uint32_t vst = st + C::kv_bytes;
@@ -609,19 +617,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
             if (TYPE == FT_KV_MXFP8) {  // (tokens 0-7, piece 2blk), (8-15, 2blk), (0-7, 2blk+1), (8-15, 2blk+1)
               ldm4t(b, vst + piece<C::rby>(16 * h + vrow, 2 * blk + vpc));
 #pragma unroll
-              for (int x = 0; x < 4; ++x)  // bytes t0d0 t0d1 t1d0 t1d1 -> (t0d0, t1d0), (t0d1, t1d1)
-                e4m3x4_f16(__byte_perm(b[x], 0, 0x3120), f[2 * (x >> 1)][x & 1], f[2 * (x >> 1) + 1][x & 1]);
+              for (int x = 0; x < 4; ++x) {  // bytes t0d0 t0d1 t1d0 t1d1 -> (t0d0, t1d0), (t0d1, t1d1)
+                f[2 * (x >> 1)][x & 1] = e4m3_bits<false>(b[x]);
+                f[2 * (x >> 1) + 1][x & 1] = e4m3_bits<true>(b[x]);
+              }
             } else {                    // piece blk of tokens 0-7 and 8-15
               ldm2t(b, vst + piece<C::rby>(16 * h + vrow, blk));
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                // four codes of token 0 (low half) and of token 1 -> bytes of both tokens' code i:
-                // codes 0 and 2 in the low half of y, 1 and 3 in the low half of z
-                const uint32_t y = b[x] & 0x0F0F0F0Fu, z = (b[x] >> 4) & 0x0F0F0F0Fu;
-                uint32_t e[4];
-                e2m1x8_f16(__byte_perm(y | (y >> 12), z | (z >> 12), 0x5140), e);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i][x] = e[i];
+              for (int x = 0; x < 2; ++x) {  // four codes of token 0 (low half) and of token 1
+                f[0][x] = e2m1_bits<0>(b[x]);
+                f[1][x] = e2m1_bits<1>(b[x]);
+                f[2][x] = e2m1_bits<2>(b[x]);
+                f[3][x] = e2m1_bits<3>(b[x]);
               }
             }
             const float2 sc[2] = {scale2(1, blk, 2 * h), scale2(1, blk, 2 * h + 1)};
@@ -631,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
 #pragma unroll
               for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of tokens 0-7, then of 8-15
                 const float* e = s[mt][2 * h + (i >> 1)] + 2 * (i & 1);
-                pa[i] = pack_f16(e[0] * sc[i >> 1].x, e[1] * sc[i >> 1].y);
+                pa[i] = pack(e[0] * sc[i >> 1].x, e[1] * sc[i >> 1].y);
               }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_f16(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
+              for (int i = 0; i < 4; ++i) mma(o[mt][4 * blk + i], pa, f[i][0], f[i][1]);
             }
           }
         }
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
           join_l[warp * RB + 16 * mt + g + 8 * h] = x;
         }
       }
-      put_rows<TYPE, D>(join_o + (warp * RB + 16 * mt) * C::opitch, C::opitch, o[mt], C::q ? ex2(ev) : 1.f, g, c);
+      put_rows<TYPE, D>(join_o + (warp * RB + 16 * mt) * C::opitch, C::opitch, o[mt], pow2(C::taken), g, c);
     }
     __syncthreads();
     constexpr int TPR = kThreads / RB, PC = D / 4 / TPR;  // threads of a row, 16-byte pieces of a thread

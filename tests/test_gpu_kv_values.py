@@ -53,3 +53,74 @@ def test_log_sums_do_not_depend_on_values(F, kind, heads, kv_heads, dim, new, le
     out, lse = call.run()
     assert np.all(np.isnan(out))
     X.check(np.zeros_like(out), lse, (np.zeros_like(out), *ref[1:]))
+
+
+def _spread_cache(F, kind, kv_heads, dim, page, n_pages, form, seed, special=()):
+    """A cache whose values' scales are far apart: from block to block of a row, from token to token, over the format's whole
+    range, or only those of the `special` slots far above all others."""
+    cache = K.Cache(F, kind, kv_heads, dim, page, n_pages, seed)
+    rng = np.random.default_rng(seed + 100)
+    shape = (n_pages, kv_heads, page, dim // 32)
+    top = 134 if kind == 1 else 140  # the largest scale code of the format
+    if form == "blocks":
+        code = np.broadcast_to(np.array([top, top - 30, top - 60, 27, top - 15, 60, top - 25, top - 1])[: dim // 32], shape)
+    elif form == "tokens":
+        code = np.where(rng.random(shape[:3]) < 0.03, top, top - 32)[..., None] + np.zeros(shape, dtype=int)
+    elif form == "range":
+        code = rng.integers(27, top + 1, shape)
+    else:
+        code = np.full(shape, top - 35)
+        for s in special:
+            code[s // page, :, s % page] = top
+    scale = np.ascontiguousarray(code).astype(np.uint8)
+    cache.scales[1].copy_(torch.from_numpy(scale))
+    cache.value[1] = K.stands_for(cache.t[1].cpu().numpy(), scale, kind)
+    return cache
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (16, 2, 256)])
+@pytest.mark.parametrize("form", ["blocks", "tokens", "range"])
+@pytest.mark.parametrize("new,length,wide", [(1, 1, 0), (1, 500, 0), (5, 300, 0), (70, 200, WIDE)])
+def test_values_of_small_scale_are_kept_beside_large_ones(F, kind, heads, kv_heads, dim, form, new, length, wide):
+    """Column by column, with single tokens (one row tile), a few (two, where there are such) and a chunk.  The smallest scale,
+    2^-100, times MXFP4's smallest element and a probability is near the end of FP32's range: `floor` as kvexact.py says."""
+    cache = _spread_cache(F, kind, kv_heads, dim, 16, -(-length // 16) + 1, form, dim + new)
+    X.Call(F, cache, heads, [new], [length], wide=wide).check(floor=length * 2.0 ** -104 * (2.0 ** -100 * 6))
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (16, 2, 256)])
+@pytest.mark.parametrize("new,length,window,wide", [(6, 200, 0, 0), (6, 200, 40, 0), (70, 200, 0, WIDE), (70, 200, 40, 0)])
+def test_large_values_that_a_row_does_not_see_change_nothing(F, kind, heads, kv_heads, dim, new, length, window, wide):
+    """The last new token, and the one before the last row's window, have values 2^35 times as large as the others: rows that
+    do not see them, column by column, and rows that do."""
+    at = [length - 1] + ([length - window - 1] if window else [])
+    cache = _spread_cache(F, kind, kv_heads, dim, 16, -(-length // 16), "special", new, at)
+    table = np.arange(-(-length // 16), dtype=np.int32)[None]
+    X.Call(F, cache, heads, [new], [length], table, window=window, wide=wide).check()
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128), (16, 2, 256)])
+@pytest.mark.parametrize("new,wide", [(1, 0), (5, 0), (70, WIDE)])
+def test_a_large_value_of_next_to_no_probability_takes_nothing_away(F, kind, heads, kv_heads, dim, new, wide):
+    """One token of values near the format's largest, whose probability is about 2^-60, beside tokens of values 2^15 smaller:
+    it adds 2^-45 of them, and their own sums keep every term."""
+    length, at = 260, 77
+    cache = _spread_cache(F, kind, kv_heads, dim, 16, 17, "special", new, [at])
+    scale = np.full((17, kv_heads, 16, dim // 32), 119, dtype=np.uint8)
+    scale[at // 16, :, at % 16] = 134
+    cache.scales[1].copy_(torch.from_numpy(scale))
+    cache.value[1] = K.stands_for(cache.t[1].cpu().numpy(), scale, kind)
+    table = np.arange(17, dtype=np.int32)[None]
+    call = X.Call(F, cache, heads, [new], [length], table, wide=wide, scale=0.01)
+    # every query has a part against the token's key that makes its score 60 log 2 smaller than the others'
+    key = cache.value[0][at // 16, :, at % 16]                        # [kv_heads][dim]
+    group = heads // kv_heads
+    q = call.q.reshape(new, kv_heads, group, dim)
+    need = -60 * np.log(2) / 0.01
+    q = q + ((need - (q * key[:, None]).sum(-1)) / (key * key).sum(-1)[:, None])[..., None] * key[:, None]
+    call.q_t.copy_(torch.from_numpy(q.reshape(new, heads, dim).astype(np.float32)).to(torch.bfloat16))
+    call.q = call.q_t.double().cpu().numpy()
+    call.check()
