@@ -884,8 +884,9 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         const bool bad = __any_sync(0xffffffffu, there && !good);
         if (bad && lane == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
         // rows to be cleared: of V whatever no row may see or that holds no token (it meets
-        // probabilities of zero, and must not be NaN), of K those of a bad page
-        const bool clear = kv ? pages != (1u << npg) - 1u || t + KT > cur.len : bad;
+        // probabilities of zero, and must not be NaN), the tokens that share a page with a window's
+        // first one among them; of K those of a bad page
+        const bool clear = kv ? pages != (1u << npg) - 1u || t + KT > cur.len || t < cur.lo : bad;
         if (!(ok = wait_all(empty + kv * NS + st, ph ^ 1u))) break;
         const uint32_t dst = ring_addr + st * C::stage;
         const uint32_t fb = bar(full + kv * NS + st), lb = clear ? bar(aux + kv) : fb;
@@ -906,7 +907,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
           if (!(ok = wait_all(aux + kv, aux_ph))) break;
           aux_ph ^= 1u;
           for (int r = lane; r < KT; r += 32)
-            if (!((pages >> (r >> shift)) & 1u) || t + r >= cur.len)
+            if (!((pages >> (r >> shift)) & 1u) || t + r >= cur.len || t + r < cur.lo)
               for (int i = 0; i < 8 * C::panels; ++i)
                 *reinterpret_cast<uint4*>(ring + (kv * NS + st) * C::stage + (i >> 3) * PANEL + r * 128 + (i & 7) * 16) =
                     make_uint4(0, 0, 0, 0);

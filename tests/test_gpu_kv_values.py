@@ -124,3 +124,31 @@ def test_a_large_value_of_next_to_no_probability_takes_nothing_away(F, kind, hea
     call.q_t.copy_(torch.from_numpy(q.reshape(new, heads, dim).astype(np.float32)).to(torch.bfloat16))
     call.q = call.q_t.double().cpu().numpy()
     call.check()
+
+
+# Heads, cache heads, head width and new tokens of chunks with a window that are much work all the same.
+WINDOWED = [(64, 2, 64, 600), (64, 1, 128, 400), (32, 1, 256, 400)]
+
+
+@pytest.mark.parametrize("kind,copies", [(0, True), (1, True), (1, False), (2, True), (2, False)])
+@pytest.mark.parametrize("heads,kv_heads,dim,new", WINDOWED + [(4, 1, 64, 4), (8, 1, 128, 3), (16, 2, 256, 1)])
+@pytest.mark.parametrize("page,window", [(16, 50), (64, 50), (128, 301)])
+def test_tokens_before_every_window_do_not_matter(F, kind, copies, heads, kv_heads, dim, new, page, window):
+    """Keys and values of the tokens before the first row's window are no numbers, some of them in the window's first page."""
+    length = new + 700
+    first = length - new - window + 1  # the first token that any row sees
+    pages = -(-length // page)
+    cache = K.Cache(F, kind, kv_heads, dim, page, pages, 8)
+    table = np.arange(pages, dtype=np.int32)[None]
+    call = X.Call(F, cache, heads, [new], [length], table, window=window, copies=copies)
+    ref = call.reference(lambda s, i: i < 8 or i % 37 == 0)
+    assert first % page
+    for j in range(first - 40, first):
+        for i in (0, 1):
+            if kind == 0:
+                cache.t[i][j // page, :, j % page] = float("nan") if j % 3 else float("inf")
+            else:
+                cache.scales[i][j // page, :, j % page] = 255
+    got = call.run()
+    assert call.word.item() == 0
+    X.check(*got, ref)
