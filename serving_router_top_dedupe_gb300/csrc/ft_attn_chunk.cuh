@@ -18,10 +18,11 @@
 // Bound by the tensor core together with shared memory: a step of two row tiles is 32 MMAs of 64
 // clocks, which read 128 bytes a clock of operands while the next tiles are written, and takes
 // about 3500 clocks (84 for an MMA; the rest is between batches of MMAs, whose queue holds three).
-// With 64-wide heads the softmax is as long as the products.
+// With 64-wide heads the softmax is as long as the products; with 256-wide ones every CTA's row tile
+// takes all of K and V out of L2, 128 KB a tile and SM, and that bounds it over long caches.
 // Measured: 8192 new tokens, 32 query heads over 4 of 128, BF16: 466 us = 1181 TFLOP/s; 2048 over
-// 65536 (MXFP8, decoded once): 1630-1680 us = 1300; 500 over 100001, heads of 256: 652-673 us =
-// 1215-1255.  Quantised pages decoded where they are read, 512 rows over 16 x 8192 tokens of 4 x 128:
+// 65536 (MXFP8, decoded once): 1630-1680 us = 1300; 500 over 100001, heads of 256: 705 us =
+// 1158.  Quantised pages decoded where they are read, 512 rows over 16 x 8192 tokens of 4 x 128:
 // MXFP8 197 us, MXFP4 179, BF16 142: there the decoding warps bound it.
 //
 // Warps 0-3 (and 4-7): softmax, output.  Then one warp that issues every MMA, and the loaders:
@@ -53,12 +54,7 @@ template <int TYPE, int D>
 struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
   static constexpr int tiles = D <= 128 ? 2 : 1;
-  // Two CTAs of a cluster share one item of 256 rows, a row tile each, and the loads of its K and
-  // V: each loads half a tile into both.  With 256-wide heads (one row tile per CTA) the loads out
-  // of L2 would bound the kernel otherwise: 128 KB for a tile and SM, 9.5 TB/s (500 tokens over 100001
-  // 690 us, with pairs 651).
-  static constexpr bool pair = !q && tiles == 1;
-  static constexpr int RB = 128 * tiles * (pair ? 2 : 1);
+  static constexpr int RB = 128 * tiles;
   // Counts of an item besides its tiles: loading queries, joining and storing outputs (8192 new
   // tokens: 0 746 us, 3 463, 8 476).
   static constexpr int OV = D == 64 ? 5 : 3;
@@ -104,17 +100,6 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// The same barrier in both CTAs of a pair.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -230,15 +215,6 @@ __device__ __forceinline__ uint32_t multiplier(uint32_t code) {
   return mul2((code << 7 | (code + 1) >> 8) * 0x00010001u, lack);
 }
 
-// Into both CTAs of a pair, at the same place, completing on the same barrier of each.
-__device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
-      : "memory");
-}
-
 // 16 bytes of codes -> 16 (MXFP8) or 32 (MXFP4) BF16 values in their order.
 template <int TYPE>
 __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
@@ -352,7 +328,7 @@ __device__ __forceinline__ void raw_store(uint8_t* stage, int lt, const Raw<TYPE
 }
 
 template <int TYPE, int D>
-__global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_bounds__(Cfg<TYPE, D>::threads, 1)
+__global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     attn_chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   using C = Cfg<TYPE, D>;
   constexpr int NS = C::stages, T = C::tiles;
@@ -379,7 +355,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
   if (tid == 0) {
     for (int s = 0; s < 2 * NS; ++s) {
       ptx::mbar_init(bar(full + s), C::q ? 4 : 1);
-      ptx::mbar_init(bar(empty + s), C::pair ? 2 : 1);
+      ptx::mbar_init(bar(empty + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(q_full + i), 128);
@@ -395,11 +371,9 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
   pdl_wait();
   pdl_trigger();
   if (p.have && __ldg(p.have) != p.want) return;
-  const int cta = C::pair ? blockIdx.x >> 1 : blockIdx.x, ctas = C::pair ? gridDim.x >> 1 : gridDim.x;
-  const int rank = C::pair ? blockIdx.x & 1 : 0;  // row tile of this CTA (a pair)
   ChunkWalk<TYPE, D> wk;
   long long per;
-  if (!plan<C::RB, KT, C::OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), cta, ctas, kJoin, wk, per)) return;
+  if (!plan<C::RB, KT, C::OV, C::threads>(p, *reinterpret_cast<PlanSmem*>(ring), blockIdx.x, gridDim.x, kJoin, wk, per)) return;
   if (warp == C::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(tmem_slot))
                  : "memory");
@@ -408,7 +382,6 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
   fence_async();  // the ring held the plan: copies may write it now
   tc_before();
   __syncthreads();
-  if (C::pair) cluster_sync();  // the other CTA's barriers are there
   tc_after();
   const uint32_t tmem = *tmem_slot, q_addr = ptx::smem_u32(smem);
   auto wait = [&](uint64_t* b, uint32_t parity) { return ptx::mbar_wait(bar(b), parity, abort_flag, p.error_word); };
@@ -420,8 +393,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
   if (warp < C::soft_warps) {
     // ------------------------------------------------------------------ softmax and output
     if (C::split) regs_up<C::soft_regs>();
-    const int rt = warp >> 2;              // row tile in this CTA
-    const int tile = C::pair ? rank : rt;  // of the block
+    const int rt = warp >> 2;              // row tile
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t o_tm = tl + C::o_col + rt * D;
@@ -431,10 +403,10 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
 
     // an item's queries into shared memory, once no product reads the last ones
     auto load_q = [&](const Cursor& cur) {
-      const int rows = rows_of(cur, tile);
-      if (!C::pair && rows <= 0) return;  // a pair's second CTA goes along with zeros
+      const int rows = rows_of(cur, rt);
+      if (rows <= 0) return;
       constexpr int PQ = D / 8;  // 16-byte pieces of a row
-      const int row0 = cur.rb * C::RB + 128 * tile, wt = tid & 127;
+      const int row0 = cur.rb * C::RB + 128 * rt, wt = tid & 127;
       const uint16_t* src = p.q + (long long)cur.q0 * p.q_stride + (long long)cur.head * p.group * D;
       const uint32_t dst = q_addr + rt * C::stage;
       auto at = [&](int u) {
@@ -470,7 +442,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
       for (int i = 0; i < 8; ++i) {
         const int x = 4 * i + (lane >> 3), row = (warp & 3) * 32 + x, pc = lane & 7;
         if (row < rows) {
-          const int rr = cur.rb * C::RB + 128 * tile + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
+          const int rr = cur.rb * C::RB + 128 * rt + row, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
           *reinterpret_cast<uint4*>(p.out + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D + col + pc * 8) =
               *reinterpret_cast<const uint4*>(stg + x * 128 + ((pc ^ (x & 7)) << 4));
         }
@@ -485,8 +457,8 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
     load_q(wk.cur);
     while (ok && wk.more()) {  // one item
       const Cursor cur = wk.cur;
-      const int rows = rows_of(cur, tile);
-      const int rbase = cur.rb * C::RB + 128 * tile;
+      const int rows = rows_of(cur, rt);
+      const int rbase = cur.rb * C::RB + 128 * rt;
       // what this row sees: [lo, hi); what every row of the tile sees: [lo_max, hi_min)
       int lo = 0, hi = 1 << 30, lo_max = 0, hi_min = 1 << 30;
       if (rows > 0) {
@@ -505,7 +477,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
       const int steps = (int)(wk.end() - wk.w);
       int t = wk.tile() * KT;
       const int t_first = t;
-      for (int j = 0; j < steps && (C::pair || rows > 0); ++j, ++step, t += KT) {
+      for (int j = 0; j < steps && rows > 0; ++j, ++step, t += KT) {
         const int u = T == 2 ? rt : (int)(step & 1);
         const uint32_t s_tm = tl + 128 * u;
         if (!(ok = wait_all(s_full + u, (s_ph >> u) & 1))) break;
@@ -663,7 +635,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         if (lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       } else {
         // partial result: columns in groups of four, the rows of a group side by side
-        const int me = cta, at = 128 * tile + r;
+        const int me = blockIdx.x, at = 128 * rt + r;
         float* slot = p.partials + (size_t)(2 * me + (me == ca ? 1 : 0)) * C::slot_floats;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -680,7 +652,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         __stcg(slot + C::RB * (D + 1) + at, l);
         __syncwarp();
         redo([&](int x, const float* again) {
-          const int row = 128 * tile + (warp & 3) * 32 + x;
+          const int row = 128 * rt + (warp & 3) * 32 + x;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const int d = lane * (D / 32) + i;
@@ -688,7 +660,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
           }
         });
         // each warp joins its own 32 rows: the last CTA's warp to come, in the parts' order
-        uint32_t* counter = p.counters + 8 * ca + 4 * tile + (warp & 3);
+        uint32_t* counter = p.counters + 8 * ca + 4 * rt + (warp & 3);
         __syncwarp();
         int is_last = 0;
         if (lane == 0) {  // with the warp's barriers, one lane's fences order all its accesses
@@ -785,10 +757,6 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         tc_after();
         return true;
       };
-      auto release = [&](uint64_t* b) {
-        if (C::pair) commit_pair(bar(b));
-        else commit(bar(b));
-      };
       auto nothing = [] {};
       // The issuing thread must not keep the tensor core waiting, whose queue holds about three
       // MMAs: what changes from item to item is worked out between items, and waits and releases
@@ -806,7 +774,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
           if (!(ok = wait_q(1))) break;
           scores(1, 1, nothing);
         }
-        release(empty + kst);
+        commit(bar(empty + kst));
         advance(kst, kph);
         bool p_there = false;  // of the second row tile, seen ahead of time
         for (int j = 0; j < n; ++j) {
@@ -815,7 +783,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
             if (!(ok = wait(full + NS + vst, vph) && (!more || wait(full + kst, kph)) && wait_p(0))) break;
             product(0, 0, j == 0, !more, nothing);
             auto let_v_go = [&] {
-              release(empty + NS + vst);
+              commit(bar(empty + NS + vst));
               advance(vst, vph);
             };
             if (two) {
@@ -830,7 +798,7 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
             }
             if (more) {
               scores(two, two, let_v_go);
-              release(empty + kst);
+              commit(bar(empty + kst));
               advance(kst, kph);
             } else {
               let_v_go();
@@ -840,12 +808,12 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
               if (!(ok = wait(full + kst, kph))) break;
               tc_after();
               scores(0, u ^ 1, nothing);
-              release(empty + kst);
+              commit(bar(empty + kst));
               advance(kst, kph);
             }
             if (!(ok = wait(full + NS + vst, vph) && wait_p(u))) break;
             product(0, u, j == 0, !more, nothing);
-            release(empty + NS + vst);
+            commit(bar(empty + NS + vst));
             advance(vst, vph);
             u ^= 1;
           }
@@ -892,17 +860,9 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
         const uint32_t fb = bar(full + kv * NS + st), lb = clear ? bar(aux + kv) : fb;
         if (lane == 0) ptx::mbar_arrive_expect_tx(lb, __popc(pages) * ps * 128 * C::panels);
         __syncwarp();
-        if constexpr (C::pair) {
-          // this CTA's half of the tile's rows, in copies of up to 64 rows and 64 columns, to both
-          const int bs = min(ps, 64), copies = 64 / bs, from = 64 * rank + bs * (lane % copies), pn = lane / copies;
-          const int id = __shfl_sync(0xffffffffu, page, from >> shift);
-          if (pn < C::panels && ((pages >> (from >> shift)) & 1u))
-            tma2d_pair(dst + pn * PANEL + from * 128, map, 64 * pn,
-                       ((id * p.n_kv_heads + cur.head) << shift) + (from & (ps - 1)), lb);
-        } else if (good && panel < C::panels) {
+        if (good && panel < C::panels)
           tma2d(dst + panel * PANEL + (pg << shift) * 128, map, 64 * panel,
                 (page * p.n_kv_heads + cur.head) << shift, lb);
-        }
         if (clear) {
           if (!(ok = wait_all(aux + kv, aux_ph))) break;
           aux_ph ^= 1u;
@@ -989,7 +949,6 @@ __global__ void __cluster_dims__(Cfg<TYPE, D>::pair ? 2 : 1, 1, 1) __launch_boun
   __syncwarp();
   tc_before();
   __syncthreads();
-  if (C::pair) cluster_sync();  // nothing of the other CTA's is on its way here any more
   if (warp == C::mma_warp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -1010,13 +969,12 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// The cache's rows as a 2-D tensor [rows][D]: boxes of `rows` rows of a page and head, 64 columns
-// wide.
-inline cudaError_t page_map(CUtensorMap* m, const void* base, int D, int rows, const AttnParams& p) {
+// The cache's rows as a 2-D tensor [rows][D]: boxes of one page and head, 64 columns wide.
+inline cudaError_t page_map(CUtensorMap* m, const void* base, int D, const AttnParams& p) {
   if (!encoder()) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)p.n_pages * p.n_kv_heads * p.page_size};
   const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)rows}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64, (cuuint32_t)p.page_size}, one[2] = {1, 1};
   const CUresult r = encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1030,14 +988,13 @@ cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
   CUtensorMap tk{}, tv{};
   cudaError_t e = cudaSuccess;
   if (!C::q) {
-    const int rows = C::pair && p.page_size > 64 ? 64 : p.page_size;
-    e = page_map(&tk, p.k, D, rows, p);
-    if (e == cudaSuccess) e = page_map(&tv, p.v, D, rows, p);
+    e = page_map(&tk, p.k, D, p);
+    if (e == cudaSuccess) e = page_map(&tv, p.v, D, p);
   }
   static std::atomic<uint64_t> ready{0};  // devices whose limit is set
   if (e == cudaSuccess) e = prepare_kernel(attn_chunk_kernel<TYPE, D>, C::smem, ready);
   if (e != cudaSuccess) return e;
-  return launch_k(attn_chunk_kernel<TYPE, D>, dim3(C::pair ? n_sm & ~1 : n_sm), dim3(C::threads), C::smem, s, true, tk, tv, p);
+  return launch_k(attn_chunk_kernel<TYPE, D>, dim3(n_sm), dim3(C::threads), C::smem, s, true, tk, tv, p);
 }
 
 template <int TYPE>
