@@ -59,8 +59,10 @@ typedef struct {
  *   k_bf16, v_bf16  dev; token t's rows [n_kv_heads][head_dim] start t * k_stride (v_stride)
  *                   elements after the pointer (parts of a wider projection's rows are
  *                   fine); pointers 16-byte aligned, strides multiples of 8
- *   slots           dev [n_tokens]; a negative slot skips its token (padding).  Two tokens
- *                   with one slot leave either's row.
+ *   slots           dev [n_tokens]; a negative slot skips its token (padding).  The others of
+ *                   a call are distinct: a row that two tokens name is undefined (parts of
+ *                   both, and codes of one with scales of the other), other rows are as they
+ *                   should be.
  *   error_word_out  optional dev uint32, into which FT_DEVERR_BAD_INDEX is OR-ed for a slot
  *                   beyond the cache (its token is skipped)
  * n_tokens = 0 does nothing.  Errors: FT_ERR_INVALID, FT_ERR_CUDA. */

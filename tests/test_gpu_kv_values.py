@@ -152,3 +152,30 @@ def test_tokens_before_every_window_do_not_matter(F, kind, copies, heads, kv_hea
     got = call.run()
     assert call.word.item() == 0
     X.check(*got, ref)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_a_slot_that_two_tokens_name_leaves_other_rows_alone(F, kind):
+    """The row itself is undefined; every other one is as without the repeated slot."""
+    heads, dim, page, n = 3, 128, 16, 40
+    rng = np.random.default_rng(2)
+    x = [torch.from_numpy(rng.standard_normal((n, heads, dim)).astype(np.float32)).to(torch.bfloat16).cuda() for _ in "kv"]
+    cache = X.Cache(F, kind, *(np.zeros((4, heads, page, dim)) for _ in "kv"))
+    slots = rng.permutation(4 * page)[:n]
+    slots[7] = slots[31]
+    on = torch.from_numpy(slots.astype(np.int32)).cuda()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    F.ft_kv_write(cache.c, *x, on, error_word=word)
+    every = [torch.empty(4 * page, heads, dim, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    F.ft_kv_read(cache.c, torch.arange(4 * page, dtype=torch.int32, device="cuda"), *every, error_word=word)
+    torch.cuda.synchronize()
+    assert word.item() == 0
+    for t, rows in zip(x, every):
+        want = np.zeros((4 * page, heads, dim))
+        a = t.double().cpu().numpy()
+        if kind:
+            code, scale = K.quantise(a, kind)
+            a = K.stands_for(K.packed(code, kind), scale, kind)
+        want[slots] = a
+        others = np.arange(4 * page) != slots[7]
+        assert np.array_equal(rows.double().cpu().numpy()[others], want[others])
