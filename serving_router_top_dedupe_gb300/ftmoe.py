@@ -395,63 +395,87 @@ def make_config(n_layers, hidden, inter, n_experts, top_k, has_shared, wtype, ma
 
 
 # ----------------------------------------------- paged key/value cache (include/ft_kv.h)
-def _dense(what, t, shape, itemsize) -> None:
-    """Raises unless tensor t has this shape (None: any size), element size and C order."""
-    if t.element_size() != itemsize or t.dim() != len(shape) or not t.is_contiguous() or any(
+# The element types that stand for each kind of operand: the type itself, or its raw patterns (torch types, learnt when
+# the first cache or arguments are made: importing this module does not import torch).
+_BF16, _I32, _F32, _BYTE = set(), set(), set(), set()
+
+
+def _learn_types() -> None:
+    if not _F32:
+        import torch
+
+        for known, names in ((_BF16, ("bfloat16", "int16", "uint16")), (_I32, ("int32", "uint32")), (_F32, ("float32",)),
+                             (_BYTE, ("uint8", "int8", "float8_e4m3fn", "float8_e8m0fnu", "float4_e2m1fn_x2"))):
+            known.update(getattr(torch, n) for n in names if hasattr(torch, n))
+
+
+def _dense(what, t, shape, types) -> None:
+    """Raises unless tensor t has this shape (None: any size), one of these types and C order."""
+    if t.dtype not in types or t.dim() != len(shape) or not t.is_contiguous() or any(
             n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: expected a contiguous tensor of shape {list(shape)} with {itemsize}-byte elements, "
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {list(shape)} of {' or '.join(sorted(map(str, types)))}, "
                          f"got {list(t.shape)} of {t.dtype}")
 
 
 def _rows(what, t, n, heads, dim) -> int:
     """Token stride of t, which has to be [n][heads][dim] 16-bit rows that are each contiguous."""
     s = t.stride()
-    if t.shape != (n, heads, dim) or t.element_size() != 2 or n and (s[2] != 1 or heads > 1 and s[1] != dim):
+    if t.shape != (n, heads, dim) or t.dtype not in _BF16 or n and (s[2] != 1 or heads > 1 and s[1] != dim):
         raise ValueError(f"{what}: expected rows of [{n}][{heads}][{dim}] BF16 elements, got {list(t.shape)} of {t.dtype} "
                          f"with strides {list(s)}")
     return s[0] if n > 1 else heads * dim
 
 
+def _word(t) -> int | None:
+    """Address of an error word: a tensor of one 32-bit integer or more, an address, or None."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in _I32 or t.numel() < 1:
+        raise ValueError(f"error_word: expected an int32, got {list(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
 def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_scale=None, v_scale=None) -> ft_kv_cache:
     """One layer's cache over torch tensors that the caller keeps: k, v [n_pages][n_kv_heads][page_size][elements of
     a row] (BF16 elements, or bytes), scales [n_pages][n_kv_heads][page_size][head_dim // 32] bytes."""
+    _learn_types()
     per = {FT_KV_BF16: head_dim, FT_KV_MXFP8: head_dim, FT_KV_MXFP4: head_dim // 2}.get(kv_type)
     if per is None:
         raise ValueError(f"kv_type = {kv_type}")
     lead = (n_pages, n_kv_heads, page_size)
     for name, t in (("k", k), ("v", v)):
-        _dense(name, t, (*lead, per), 2 if kv_type == FT_KV_BF16 else 1)
+        _dense(name, t, (*lead, per), _BF16 if kv_type == FT_KV_BF16 else _BYTE)
     if kv_type == FT_KV_BF16:
         k_scale = v_scale = None
     else:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is None:
                 raise ValueError(f"{name} is missing")
-            _dense(name, t, (*lead, head_dim // 32), 1)
+            _dense(name, t, (*lead, head_dim // 32), _BYTE)
     c = ft_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
     c.tensors, c.row, c.ref = (k, v, k_scale, v_scale), (n_kv_heads, head_dim), C.byref(c)
     return c
 
 
-def _kv_rows(cache, a, b, names, slots):
-    """n, strides of both tensors: the checks that ft_kv_write and ft_kv_read share."""
+def _kv_rows(cache, a, b, names, slots, error_word):
+    """n, strides of both tensors, address of the error word: the checks that ft_kv_write and ft_kv_read share."""
     n = a.shape[0]
-    if slots.shape != (n,) or slots.element_size() != 4 or not slots.is_contiguous():
-        _dense("slots", slots, (n,), 4)
-    return n, _rows(names[0], a, n, *cache.row), _rows(names[1], b, n, *cache.row)
+    if slots.shape != (n,) or slots.dtype not in _I32 or not slots.is_contiguous():
+        _dense("slots", slots, (n,), _I32)
+    heads, dim = cache.row
+    return n, _rows(names[0], a, n, heads, dim), _rows(names[1], b, n, heads, dim), _word(error_word)
 
 
 def ft_kv_write(cache, k, v, slots, error_word=None, stream=None) -> None:
     """k, v: torch BF16 [n][n_kv_heads][head_dim], rows contiguous (parts of a wider tensor are fine); slots: int32 [n]."""
-    n, ks, vs = _kv_rows(cache, k, v, ("k", "v"), slots)
-    _check(_lib.ft_kv_write(cache.ref, n, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), _ptr(error_word), stream))
+    n, ks, vs, word = _kv_rows(cache, k, v, ("k", "v"), slots, error_word)
+    _check(_lib.ft_kv_write(cache.ref, n, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), word, stream))
 
 
 def ft_kv_read(cache, slots, k_out, v_out, error_word=None, stream=None) -> None:
     """The rows of `slots` as BF16 into k_out, v_out (laid out as ft_kv_write's k and v)."""
-    n, ks, vs = _kv_rows(cache, k_out, v_out, ("k_out", "v_out"), slots)
-    _check(_lib.ft_kv_read(cache.ref, n, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ks, vs, _ptr(error_word),
-                           stream))
+    n, ks, vs, word = _kv_rows(cache, k_out, v_out, ("k_out", "v_out"), slots, error_word)
+    _check(_lib.ft_kv_read(cache.ref, n, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ks, vs, word, stream))
 
 
 def ft_attn_workspace(n_heads, n_kv_heads, head_dim) -> int:
@@ -465,17 +489,20 @@ def make_attn_args(n_heads, max_new, q, q_start, kv_len, page_table, out, worksp
     """Arguments of ft_attn over torch tensors that the caller keeps; they can be used again while the tensors' contents
     change.  q, out: BF16 [n_tokens][n_heads][head_dim], rows contiguous; q_start int32 [n_seqs + 1]; kv_len int32
     [n_seqs]; page_table int32 [n_seqs][pages]; lse FP32 [n_tokens][n_heads] or None."""
+    _learn_types()
     n, dim = q.shape[0], q.shape[-1]
     qs, os_ = _rows("q", q, n, n_heads, dim), _rows("out", out, n, n_heads, dim)
     seqs = kv_len.shape[0]
-    _dense("kv_len", kv_len, (None,), 4)
-    _dense("q_start", q_start, (seqs + 1,), 4)
-    _dense("page_table", page_table, (seqs, None), 4)
+    _dense("kv_len", kv_len, (None,), _I32)
+    _dense("q_start", q_start, (seqs + 1,), _I32)
+    _dense("page_table", page_table, (seqs, None), _I32)
     if lse is not None:
-        _dense("lse", lse, (n, n_heads), 4)
+        _dense("lse", lse, (n, n_heads), _F32)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
     a = ft_attn_args(n_heads, n, seqs, max_new, page_table.shape[1], int(bool(causal)), window, scale, _ptr(q), qs,
                      _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(out), os_, _ptr(lse), _ptr(workspace),
-                     workspace.numel() * workspace.element_size(), _ptr(error_word))
+                     workspace.numel() * workspace.element_size(), _word(error_word))
     a.tensors, a.head_dim, a.ref = (q, q_start, kv_len, page_table, out, workspace, lse, error_word), dim, C.byref(a)
     return a
 
