@@ -435,6 +435,11 @@ def _word(t) -> int | None:
     return t.data_ptr()
 
 
+def _host(tensors) -> bool:
+    """Whether one of the tensors is not on the GPU."""
+    return any(t is not None and not isinstance(t, int) and not t.is_cuda for t in tensors)
+
+
 def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_scale=None, v_scale=None) -> ft_kv_cache:
     """One layer's cache over torch tensors that the caller keeps: k, v [n_pages][n_kv_heads][page_size][elements of
     a row] (BF16 elements, or bytes), scales [n_pages][n_kv_heads][page_size][head_dim // 32] bytes."""
@@ -454,6 +459,7 @@ def make_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, k, v, k_sca
             _dense(name, t, (*lead, head_dim // 32), _BYTE)
     c = ft_kv_cache(kv_type, n_kv_heads, head_dim, page_size, n_pages, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
     c.tensors, c.row, c.ref = (k, v, k_scale, v_scale), (n_kv_heads, head_dim), C.byref(c)
+    c.host = _host(c.tensors)
     return c
 
 
@@ -463,7 +469,10 @@ def _kv_rows(cache, a, b, names, slots, error_word):
     if slots.shape != (n,) or slots.dtype not in _I32 or not slots.is_contiguous():
         _dense("slots", slots, (n,), _I32)
     heads, dim = cache.row
-    return n, _rows(names[0], a, n, heads, dim), _rows(names[1], b, n, heads, dim), _word(error_word)
+    rows = n, _rows(names[0], a, n, heads, dim), _rows(names[1], b, n, heads, dim), _word(error_word)
+    if cache.host or not (a.is_cuda and b.is_cuda and slots.is_cuda) or error_word is not None and _host((error_word,)):
+        raise ValueError(f"the cache, {names[0]}, {names[1]}, slots and error_word have to be on the GPU")
+    return rows
 
 
 def ft_kv_write(cache, k, v, slots, error_word=None, stream=None) -> None:
@@ -504,10 +513,13 @@ def make_attn_args(n_heads, max_new, q, q_start, kv_len, page_table, out, worksp
                      _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(out), os_, _ptr(lse), _ptr(workspace),
                      workspace.numel() * workspace.element_size(), _word(error_word))
     a.tensors, a.head_dim, a.ref = (q, q_start, kv_len, page_table, out, workspace, lse, error_word), dim, C.byref(a)
+    a.host = _host(a.tensors)
     return a
 
 
 def ft_attn(cache, args, stream=None) -> None:
     if args.head_dim != cache.row[1]:
         raise ValueError(f"q has rows of {args.head_dim}, the cache of {cache.row[1]}")
+    if cache.host or args.host:
+        raise ValueError("the cache and every tensor of the arguments have to be on the GPU")
     _check(_lib.ft_attn(cache.ref, args.ref, stream))

@@ -64,3 +64,28 @@ def test_rows_of_other_types_are_refused(F, monkeypatch):
         with pytest.raises(ValueError):
             F.ft_kv_read(c, s, k, v, error_word=word)
 
+
+def test_tensors_that_are_not_on_the_gpu_are_refused(F, monkeypatch):
+    monkeypatch.setattr(F, "_lib", None)
+    seen = lambda *s, dtype: torch.zeros(*s, dtype=dtype).as_subclass(Seen)
+    x, slots = seen(3, 2, 128, dtype=torch.bfloat16), seen(3, dtype=torch.int32)
+    host = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    word = torch.zeros(1, dtype=torch.int32)
+    for cache, k, v, s, w in [(_cache(F, False), x, x, slots, None), (_cache(F), host, x, slots, None), (_cache(F), x, host, slots, None),
+                              (_cache(F), x, x, torch.zeros(3, dtype=torch.int32), None), (_cache(F), x, x, slots, word)]:
+        with pytest.raises(ValueError, match="GPU"):
+            F.ft_kv_write(cache, k, v, s, error_word=w)
+        with pytest.raises(ValueError, match="GPU"):
+            F.ft_kv_read(cache, s, k, v, error_word=w)
+    with pytest.raises(ValueError, match="GPU"):
+        F.ft_attn(_cache(F), _args(F))
+    on = {n: seen(*s, dtype=d) for n, s, d in [("q", (3, 4, 128), torch.bfloat16), ("out", (3, 4, 128), torch.bfloat16),
+                                               ("q_start", (3,), torch.int32), ("kv_len", (2,), torch.int32), ("lse", (3, 4), torch.float32),
+                                               ("page_table", (2, 4), torch.int32), ("workspace", (64,), torch.uint8), ("error_word", (1,), torch.int32)]}
+    with pytest.raises(ValueError, match="GPU"):
+        F.ft_attn(_cache(F, False), _args(F, **on))
+    for name, t in on.items():
+        with pytest.raises(ValueError, match="GPU"):
+            F.ft_attn(_cache(F), _args(F, **{**on, name: t.as_subclass(torch.Tensor)}))
+    with pytest.raises(AttributeError):  # all there: the library (taken away here) is what comes next
+        F.ft_attn(_cache(F), _args(F, **on))
