@@ -179,3 +179,61 @@ def test_a_slot_that_two_tokens_name_leaves_other_rows_alone(F, kind):
         want[slots] = a
         others = np.arange(4 * page) != slots[7]
         assert np.array_equal(rows.double().cpu().numpy()[others], want[others])
+
+
+SHAPES = [(4, 4, 64), (6, 2, 128), (7, 1, 128), (16, 2, 256), (40, 2, 64)]
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", SHAPES)
+@pytest.mark.parametrize("window", [0, 37])
+def test_every_column_of_ragged_batches(F, kind, heads, kv_heads, dim, window):
+    """Single tokens, drafts and short chunks side by side."""
+    cache = K.Cache(F, kind, kv_heads, dim, 16, 120, 3)
+    X.Call(F, cache, heads, [1, 1, 3, 1, 5, 2, 1, 40], [1, 17, 333, 64, 128, 2, 500, 260], window=window).check()
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 1, 128), (3, 1, 64), (4, 2, 256)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_every_column_of_chunks(F, kind, heads, kv_heads, dim, causal):
+    cache = K.Cache(F, kind, kv_heads, dim, 64, 30, 3)
+    X.Call(F, cache, heads, [129, 70, 200], [129, 500, 777], causal=causal, wide=WIDE).check()
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim,new,wide", [
+    (4, 1, 64, 1, 0), (8, 1, 128, 1, 0), (8, 1, 128, 4, 0), (16, 2, 256, 1, 0), (4, 1, 64, 40, WIDE), (8, 1, 128, 40, WIDE),
+    (4, 2, 256, 70, WIDE), (32, 1, 128, 40, WIDE)])
+@pytest.mark.parametrize("length", [4001, 9003])
+def test_every_tile_of_a_long_cache_counts_once(F, kind, heads, kv_heads, dim, new, wide, length):
+    """One token of every 32 has an even share of nearly all of the probability, and a one in the column of its run of tokens: a
+    lost, doubled or wrongly weighted tile of any part shows in the columns that few tokens fill."""
+    page = 32
+    pages = -(-length // page)
+    rng = np.random.default_rng(length)
+    k, v = rng.standard_normal((pages, kv_heads, page, dim)) * 0.01, np.zeros((pages, kv_heads, page, dim))
+    per = -(-pages // dim)  # marked tokens of a column
+    for j, off in enumerate(rng.integers(0, page, pages)):
+        k[j, :, off] = 1.0
+        v[j, :, off, j // per] = 1.0
+    table = rng.permutation(pages).astype(np.int32)
+    back = np.argsort(table)
+    cache, table = X.Cache(F, kind, k[back], v[back]), table[None]
+    q = np.ones((new, heads, dim)) + rng.standard_normal((new, heads, dim)) * 0.01
+    keep = {0, new // 2, new - 1}
+    call = X.Call(F, cache, heads, [new], [length], table, scale=24 / dim, q=q, wide=wide)
+    call.check(rows=lambda s, i: i in keep)
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("heads,kv_heads,dim,page", [(16, 2, 256, 128), (32, 4, 128, 64), (24, 8, 64, 16)])
+def test_every_column_of_both_kernels_agrees(F, kind, heads, kv_heads, dim, page):
+    """The kernels for few and for many rows over several thousand tokens, each within its bound of the definition."""
+    cache = K.Cache(F, kind, kv_heads, dim, page, 6001 // page + 400 // page + 2, 3)
+    keep = {(0, 0), (0, 250), (0, 499), (1, 0), (1, 32)}
+    few, many = (X.Call(F, cache, heads, [500, 33], [6001, 400], max_new=m) for m in (1, 500))
+    ref = few.reference(lambda s, i: (s, i) in keep)
+    for call in (few, many):
+        X.check(*call.run(), ref)
+        assert call.word.item() == 0
