@@ -62,7 +62,9 @@ class Layers:
             self.caches.append(F.make_kv_cache(kind, KV_HEADS, DIM, PAGE, pages, k, v, *sc))
         # pages in an order of their own, as a session gets them from a pool
         self.table = torch.randperm(pages, generator=g, device="cuda").int()[None].contiguous()
-        self.workspace = torch.zeros(F.ft_attn_workspace(HEADS, KV_HEADS, DIM), dtype=torch.uint8, device="cuda")
+        # chunks have fewer than 1024 rows of a cache head here: no room for decoded pages
+        self.workspace = torch.empty(F.ft_attn_workspace(HEADS, KV_HEADS, DIM) - F.FT_ATTN_COPY_BYTES, dtype=torch.uint8, device="cuda")
+        self.workspace[:F.FT_ATTN_CLEAR_BYTES].zero_()
         self.kv_len = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.error = torch.zeros(1, dtype=torch.int32, device="cuda")
 

@@ -113,13 +113,16 @@ typedef struct {
 } ft_attn_args;
 
 /* Bytes of workspace that ft_attn uses on the current device, for any batch.  The caller sets
- * the workspace to zero once, before its first use; every call leaves it ready for the next
- * (after FT_DEVERR_TIMEOUT, a wait inside a kernel that ran out, it is to be set to zero again, and
- * the call's outputs are not to be used).  Calls that may overlap on the GPU need workspaces of
- * their own.  The last FT_ATTN_COPY_BYTES hold decoded pages of a quantised cache under chunks of
- * many rows; a workspace without them is taken too, and the pages are then decoded where they are
- * read, for every 256 rows again.
+ * the first FT_ATTN_CLEAR_BYTES of it to zero once, before its first use (what the rest holds does
+ * not matter); every call leaves it ready for the next (after FT_DEVERR_TIMEOUT, a wait inside a
+ * kernel that ran out, they are to be set to zero again, and the call's outputs are not to be
+ * used).  Calls that may overlap on the GPU need workspaces of their own.  The last
+ * FT_ATTN_COPY_BYTES hold decoded pages of a quantised cache under chunks of many rows: callers
+ * without such chunks (a BF16 cache, or fewer than 1024 rows of a cache head in a call) do not need
+ * them.  A workspace without them is taken for any call, and such chunks' pages are then decoded
+ * where they are read, for every 256 rows again.
  * Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+#define FT_ATTN_CLEAR_BYTES ((size_t)16384)
 #define FT_ATTN_COPY_BYTES (((size_t)512 << 20) + 4352)
 ft_status ft_attn_workspace(int n_heads, int n_kv_heads, int head_dim, size_t* bytes_out);
 

@@ -33,7 +33,9 @@ int sm_count() {
 }
 
 // Counters, a stand-in for the caller's error word, and two partial results for each CTA: of
-// head_dim + 2 floats for 16 rows (few rows: two CTAs per SM), or 256 or 128 rows (chunks: one).
+// head_dim + 2 floats for 16 rows (few rows: up to three CTAs per SM) or 32 (two), or for 256 or
+// 128 rows (chunks: one).
+static_assert(kCounterBytes == FT_ATTN_CLEAR_BYTES, "what the caller clears");
 size_t partial_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * (D == 256 ? 128 : 256) * (D + 2) * 4; }
 
 // What a call cannot do without; then, for the decoded copy of a quantised cache's pages: where

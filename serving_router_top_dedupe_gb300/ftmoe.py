@@ -28,6 +28,7 @@ FT_INJECT_MALLOC, FT_INJECT_REGISTER = 1, 2
 FT_HOST_PINNED, FT_HOST_HUGE_PAGES = 0, 1
 FT_KV_BF16, FT_KV_MXFP8, FT_KV_MXFP4 = 0, 1, 2
 FT_DEVERR_BAD_INDEX = 0x10
+FT_ATTN_CLEAR_BYTES, FT_ATTN_COPY_BYTES = 16384, (512 << 20) + 4352
 
 PROFILE_KINDS = ("control", "fill", "gate_up", "down_combine", "prefill_route", "prefill_gemm_gate_up",
                  "prefill_combine", "prefill_copy", "prefill_gemm_down", "router")
@@ -488,6 +489,8 @@ def ft_kv_read(cache, slots, k_out, v_out, error_word=None, stream=None) -> None
 
 
 def ft_attn_workspace(n_heads, n_kv_heads, head_dim) -> int:
+    """Bytes of a workspace for any batch.  Its first FT_ATTN_CLEAR_BYTES have to be zero before its first use; the last
+    FT_ATTN_COPY_BYTES can be left out (include/ft_kv.h says who needs them)."""
     n = C.c_size_t()
     _check(_lib.ft_attn_workspace(n_heads, n_kv_heads, head_dim, C.byref(n)))
     return n.value

@@ -237,3 +237,19 @@ def test_every_column_of_both_kernels_agrees(F, kind, heads, kv_heads, dim, page
     for call in (few, many):
         X.check(*call.run(), ref)
         assert call.word.item() == 0
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads,dim,new,lens,wide", [
+    (0, 8, 1, 128, [1, 1], [4000, 30], 0), (1, 8, 1, 128, [1, 5], [4000, 30], 0), (2, 16, 2, 256, [3, 1], [700, 90], 0),
+    (0, 8, 1, 128, [60, 1], [900, 50], WIDE), (1, 32, 1, 128, [60, 1], [900, 50], WIDE), (2, 16, 2, 256, [40, 3], [300, 20], WIDE)])
+def test_only_the_counters_of_a_workspace_need_to_be_cleared(F, kind, heads, kv_heads, dim, new, lens, wide):
+    """Bytes that are no numbers everywhere else: the same bits, also on the second call."""
+    cache = K.Cache(F, kind, kv_heads, dim, 16, sum(-(-n // 16) for n in lens), 6)
+    call = X.Call(F, cache, heads, new, lens, wide=wide)
+    want = call.run()
+    call.ws.fill_(0xFF)
+    call.ws[:F.FT_ATTN_CLEAR_BYTES].zero_()
+    for _ in range(2):
+        call.out.fill_(77.0)
+        assert all(np.array_equal(a, b) for a, b in zip(call.run(), want))
+    assert call.word.item() == 0 and call.ws[:F.FT_ATTN_CLEAR_BYTES].max().item() == 0

@@ -89,3 +89,13 @@ def test_tensors_that_are_not_on_the_gpu_are_refused(F, monkeypatch):
             F.ft_attn(_cache(F), _args(F, **{**on, name: t.as_subclass(torch.Tensor)}))
     with pytest.raises(AttributeError):  # all there: the library (taken away here) is what comes next
         F.ft_attn(_cache(F), _args(F, **on))
+
+
+def test_the_constants_are_those_of_the_header(F):
+    import os
+    import re
+
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ft_kv.h")) as f:
+        text = f.read().replace("(size_t)", "")
+    for name in ("FT_ATTN_CLEAR_BYTES", "FT_ATTN_COPY_BYTES"):
+        assert eval(re.search(rf"#define {name} (.*)", text)[1]) == getattr(F, name)
