@@ -48,7 +48,7 @@ static_assert(kStageHead == 4352, "the copy's part of the workspace");
 // From this many rows of a head on, a quantised cache's pages are decoded once into a BF16 copy;
 // below it each block of 256 rows decodes what it reads.  Both sides measured (us, decoded where
 // it is read / copied; 16 query heads over 4 cache heads of 128, 16 sequences of 4096 tokens):
-// MXFP8 512 rows 119 / 136, 1024 197 / 183, 2048 347 / 285; MXFP4 107 / 126, 179 / 175, 314 / 275.
+// MXFP8 512 rows 117 / 136, 1024 193 / 183, 2048 332 / 287; MXFP4 105 / 128, 179 / 175, 316 / 277.
 constexpr int kStageRows = 1024;
 
 // Tokens of the cache that a sequence's new ones may see, at most (its length is not known here).
@@ -58,26 +58,26 @@ long long may_see(const AttnParams& p, long long rows) {
 }
 
 // Whether the few-row kernel takes a batch (rows: of one cache head of a sequence, at most).  It
-// re-reads the cache for every 16 or 32 rows; the chunk kernel does so for every 256, but takes
+// re-reads the cache for every 16 or 32 rows; the chunk kernel does so for every 128 or 256, but takes
 // 12 us longer to start and to end, and decodes a quantised cache's tokens at about half the
 // few-row kernel's rate.  Measured with 16 sequences of 8192 tokens and 4 cache heads (us, few-row
-// kernel / chunk kernel):
+// kernel / chunk kernel, one launch each):
 //              16 rows      32 rows      48 rows     64 rows    128 rows
-//   BF16  64   44 / 62      62 / 62      79 / 62     97 / 62    156 / 62
-//   BF16 128   68 / 83     107 / 83     144 / 83    181 / 83    316 / 85
-//   BF16 256  100 / 152    174 / 152    249 / 152   329 / 152   615 / 152
-//   MXFP8 64   31 / 76      44 / 76      58 / 76     70 / 76    126 / 76
-//   MXFP8 128  48 / 115     64 / 115     93 / 115   109 / 115   197 / 115
-//   MXFP8 256  79 / 197    126 / 197    173 / 197   216 / 197   400 / 199
-//   MXFP4 64   31 / 73      44 / 73      58 / 73     70 / 74    128 / 72
-//   MXFP4 128  42 / 103     64 / 103     87 / 103   107 / 103   197 / 105
-//   MXFP4 256  70 / 179    115 / 179    162 / 179   205 / 179   390 / 179
+//   BF16  64   44 / 62      62 / 62      79 / 60     97 / 62    156 / 62
+//   BF16 128   66 / 81     107 / 83     142 / 83    177 / 83    302 / 85
+//   BF16 256  100 / 113    178 / 115    251 / 115   326 / 115   603 / 118
+//   MXFP8 64   33 / 76      46 / 76      60 / 76     74 / 76    134 / 76
+//   MXFP8 128  46 / 105     68 / 105     95 / 105   115 / 105   210 / 105
+//   MXFP8 256  87 / 187    136 / 189    187 / 187   237 / 189   440 / 188
+//   MXFP4 64   31 / 74      44 / 72      60 / 72     72 / 72    130 / 72
+//   MXFP4 128  44 / 93      64 / 93      89 / 94    109 / 93    201 / 93
+//   MXFP4 256  72 / 169    120 / 171    165 / 169   212 / 171   398 / 169
 // which is the first rule.  The second: where there is little to do in all, the shorter start
-// decides whatever the rows (one sequence of 4096 tokens, 64 rows: BF16 19 / 36, MXFP8 23 / 54,
-// MXFP4 21 / 50 with heads of 128; BF16 25 / 46 with heads of 256).  The lengths are not known
+// decides whatever the rows (one sequence of 4096 tokens, 64 rows: BF16 19 / 33, MXFP8 23 / 51,
+// MXFP4 23 / 48 with heads of 128; BF16 27 / 42 with heads of 256).  The lengths are not known
 // here; what the tables and the window allow bounds them.
 bool takes_few(const AttnParams& p, int type, int D, long long rows) {
-  if (rows <= (type == FT_KV_BF16 ? 16 : D == 256 ? 48 : 64)) return true;
+  if (rows <= (type == FT_KV_BF16 ? 16 : D == 64 ? 64 : 48)) return true;
   const long long tokens = (long long)p.n_tokens * p.group;
   const long long blocks = std::min(p.n_seqs * ((rows + 31) / 32), tokens / 32 + p.n_seqs);  // of 32 rows
   const double work = (double)blocks * p.n_kv_heads * may_see(p, rows) * D;  // the two meet at 0.13 to 0.5 of 2^27
@@ -87,13 +87,15 @@ bool takes_few(const AttnParams& p, int type, int D, long long rows) {
 // Whether a batch's sequences of few rows (single tokens, mostly) get a launch of the few-row
 // kernel of their own, before the one for the others: sequences of different numbers of new tokens,
 // and much to read.  Measured (us, one launch / two), one chunk besides single tokens that each see
-// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 142 / 97, 4 x 128 117 / 120,
-// 2 x 256 132 / 144; 31 and a chunk of 512 over 2048: MXFP8 350 / 121, 300 / 134, 313 / 148, MXFP4
-// 312 / 121, 270 / 121, 288 / 140, BF16 191 / 154, 152 / 159, 165 / 173; 63 and a chunk of 1024 over
-// 8192: MXFP8 590 / 229, 477 / 276, 587 / 288, BF16 449 / 281, 349 / 318, 359 / 318.  With little to
-// read the second launch costs more than it saves (7 that see 1000 and a chunk of 1024: 57 / 86).
+// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 144 / 99, 4 x 128 117 / 121,
+// 2 x 256 129 / 148; 31 and a chunk of 512 over 2048: MXFP8 339 / 126, 294 / 132, 271 / 152, MXFP4
+// 304 / 123, 267 / 123, 242 / 140; 63 and a chunk of 1024 over 8192: MXFP8 586 / 237, 476 / 274,
+// 587 / 286, BF16 425 / 284, 328 / 316, 263 / 306: over a BF16 cache of 256-wide heads both kernels
+// read a block's tokens at about the same rate, and one launch does.  With little to read the second
+// launch costs more than it saves (7 that see 1000 and a chunk of 1024: 57 / 86).
 constexpr int kFewRows = 16;
 bool splits(const AttnParams& p, int type, int D, long long rows, int max_new) {
+  if (type == FT_KV_BF16 && D == 256) return false;
   return p.n_tokens < (long long)p.n_seqs * max_new &&
          (double)p.n_seqs * p.n_kv_heads * may_see(p, rows) * D >= (type == FT_KV_BF16 ? 1 << 28 : 1 << 26);
 }
