@@ -33,6 +33,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "ft_attn_masked.cuh"
 #include "ft_attn_rows.cuh"
 #include "ft_ptx.cuh"
 
@@ -66,7 +67,7 @@ struct Cfg {
   static constexpr int threads = 32 * (soft_warps + (q ? 12 : 4));
   static constexpr int qbytes = tiles * stage;
   static constexpr int out_bytes = soft_warps * 32 * 128;  // 64 output columns of each warp's rows
-  static constexpr int walks = q ? 8 * 96 : 0;             // where the loaders' walks wait
+  static constexpr int walks = q ? 8 * 112 : 0;            // where the loaders' walks wait
   static constexpr int smem = 1024 + qbytes + 2 * stages * stage + out_bytes + 512 + walks;
   // Registers of the softmax, MMA and loader warps out of those that the block starts with:
   // BF16, two tiles (168 x 384 = 64512): 216 x 256 + 72 x 128 = 64512;
@@ -246,15 +247,21 @@ __device__ __forceinline__ void decode16(uint4 w, uint32_t scale, uint4* out) {
 // What a loader keeps of an item while it is at it (the rest of its walk waits in shared memory).
 struct Part {
   const int32_t* table;  // the sequence's row of the page table
-  int len, lo, head;
+  int lo, hi, head;
   int t, left;           // first token of the next tile, tiles left in this CTA's part of the item
 };
+
+// A loader notes, before it hands a tile on, that values that are not finite were left out of the
+// item with this number (of the CTA's items).  The place is shared with items 8, 16, ... later, so
+// a row that comes late may be told so for nothing, which does no harm, but never misses it.
+__device__ __forceinline__ void note(volatile uint32_t* found, uint32_t item) { found[item & 7] = item + 1; }
+__device__ __forceinline__ bool noted(const volatile uint32_t* found, uint32_t item) { return found[item & 7] > item; }
 
 // Page ids of a tile: lane i (and i + 8, ...) holds that of tokens [t + 16 i, t + 16 i + 16), or
 // -1 where no row sees them.
 __device__ __forceinline__ int tile_pages(const AttnParams& p, const Part& it, int t, int lane) {
   const int tok = t + 16 * (lane & 7);
-  if (tok >= it.len || tok + 16 <= it.lo) return -1;
+  if (tok >= it.hi || tok + 16 <= it.lo) return -1;
   const int page = __ldg(it.table + (tok >> p.page_shift));
   if ((unsigned)page < (unsigned)p.n_pages) return page;
   atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
@@ -264,7 +271,8 @@ __device__ __forceinline__ int tile_pages(const AttnParams& p, const Part& it, i
 // 16-byte pieces of a tile's codes that one loader thread holds: piece lt % PR of rows
 // (lt + 128 i) / PR.  A warp's pieces belong to 32 rows, and lane l holds the scale codes of
 // the l-th of them (zero where nothing is seen: the codes loaded for such a row, from some
-// other place of the cache, then stand for zeros).
+// other place of the cache, then stand for zeros).  some: the tokens outside of which only some
+// rows see (of values; NULL for keys).  True: scales that stand for NaN were left out.
 template <int TYPE, int D>
 struct Raw {
   static constexpr int PR = row_bytes(TYPE, D) / 16;  // pieces of a row, and of a thread
@@ -273,8 +281,8 @@ struct Raw {
 };
 
 template <int TYPE, int D>
-__device__ __forceinline__ void raw_load(const AttnParams& p, const Part& it, int t, int pages, const uint8_t* base,
-                                         const uint8_t* scales, int lt, Raw<TYPE, D>& x) {
+__device__ __forceinline__ bool raw_load(const AttnParams& p, const Part& it, int t, int pages, const uint8_t* base,
+                                         const uint8_t* scales, const int* some, int lt, Raw<TYPE, D>& x) {
   constexpr int PR = Raw<TYPE, D>::PR;
   const int lane = lt & 31, in_page = p.page_size - 1;
   auto row_at = [&](int r, int page) {  // row of the cache; a page that is not there: some row
@@ -289,7 +297,7 @@ __device__ __forceinline__ void raw_load(const AttnParams& p, const Part& it, in
   constexpr int per = 32 / PR;  // rows of a warp's piece i
   const int r = ((lt & ~31) + 128 * (lane / per)) / PR + lane % per;
   const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
-  const bool seen = page >= 0 && t + r < it.len && t + r >= it.lo;
+  const bool seen = page >= 0 && t + r < it.hi && t + r >= it.lo;
   const uint8_t* src = scales + (size_t)(uint32_t)row_at(r, page) * (D / 32);
   if constexpr (D == 64) {
     const uint32_t s = __ldg(reinterpret_cast<const uint16_t*>(src));
@@ -302,6 +310,14 @@ __device__ __forceinline__ void raw_load(const AttnParams& p, const Part& it, in
     x.sc[0] = seen ? s.x : 0u;
     x.sc[1] = seen ? s.y : 0u;
   }
+  bool found = false;
+  if (some && (t < some[0] || t + KT > some[1])) {
+    if (t + r < some[0] || t + r >= some[1]) {
+      found = keep_finite(x.sc[0]);
+      if constexpr (D == 256) found |= keep_finite(x.sc[1]);
+    }
+  }
+  return found;
 }
 
 template <int TYPE, int D>
@@ -347,8 +363,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
   uint64_t* done = q_full + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 11);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* found = tmem_slot + 2;  // [8]
   uint8_t* walks = reinterpret_cast<uint8_t*>(bars) + 512;
-  static_assert(sizeof(ChunkWalk<TYPE, D>) <= 96, "a walk's place");
+  static_assert(sizeof(ChunkWalk<TYPE, D>) <= 96, "a walk's place, and two integers");
   auto bar = [](uint64_t* b) { return ptx::smem_u32(b); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -366,6 +383,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     }
     ptx::mbar_init(bar(done), 1);
     *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) found[i] = 0;
     ptx::mbar_fence_init();
   }
   pdl_wait();
@@ -451,11 +469,11 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     };
 
     uint32_t s_ph = 0, pvs = 0;  // phases of s_full (bit u); products with V so far
-    uint32_t items = 0;           // so far
-    uint32_t step = 0;
+    uint32_t items = 0;           // so far, of this row tile
+    uint32_t step = 0, item = 0;
     bool ok = true;
     load_q(wk.cur);
-    while (ok && wk.more()) {  // one item
+    for (; ok && wk.more(); ++item) {  // one item
       const Cursor cur = wk.cur;
       const int rows = rows_of(cur, rt);
       const int rbase = cur.rb * C::RB + 128 * rt;
@@ -583,25 +601,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       tc_after();
       int ca, cb;
       piece_owners(cur, per, ca, cb);
-      // Sums that are not finite, because of values that the row does not see?  `use` takes what
-      // is right for them: columns of a lane, row.
-      float bad = 0.f;
-      auto look = [&](const uint32_t* o) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) bad = fmaf(__uint_as_float(o[i]), 0.f, bad);
-      };
-      auto redo = [&](auto use) {
-        const int a = max(t_first, cur.lo), b = min(t, cur.len);  // the part's tokens
-        uint32_t rows_bad = __ballot_sync(0xffffffffu, bad != bad && r < rows && (lo > a || hi < b));
-        while (rows_bad) {
-          const int x = __ffs(rows_bad) - 1;
-          rows_bad &= rows_bad - 1;
-          float again[D / 32];
-          const int see_lo = __shfl_sync(0xffffffffu, lo, x), see_hi = __shfl_sync(0xffffffffu, hi, x);
-          if (redo_row<TYPE, D>(p, cur, rbase + (warp & 3) * 32 + x, see_lo, see_hi, a, b, __shfl_sync(0xffffffffu, m, x), lane, again))
-            use(x, again);
-          __syncwarp();
-        }
+      // values that were left out of the row's sums: use(column, value)
+      auto left_out = [&](auto use) {
+        if (!noted(found, item) || r >= rows) return;
+        int all_lo, all_hi;
+        all_see<C::RB>(p, cur, all_lo, all_hi);
+        not_finite<TYPE, D>(p, cur, all_lo, all_hi, lo, hi, t_first, t, use);
       };
       float* lse = nullptr;
       if (p.lse && r < rows) {
@@ -618,19 +623,16 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
             uint32_t o[32];
             tld<32>(o_tm + 64 * ch + 32 * h, o);
             tld_wait<32>(o);
-            look(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               w[16 * h + i] = pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
           }
           put_out(cur, rows, 64 * ch, w);
         }
-        redo([&](int x, const float* again) {
-          const float f = __shfl_sync(0xffffffffu, l, x) == 0.f ? 0.f : 1.f / __shfl_sync(0xffffffffu, l, x);
-          const int rr = rbase + (warp & 3) * 32 + x, tok = div_group(p, rr), hd = cur.head * p.group + rr - tok * p.group;
-          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = __float2bfloat16_rn(again[i] * f);
+        left_out([&](int d, float v) {  // the warp's rows are in memory: put_out ends with a barrier of the warp
+          const int tok = div_group(p, rbase + r), hd = cur.head * p.group + rbase + r - tok * p.group;
+          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + (long long)(cur.q0 + tok) * p.out_stride + (long long)hd * D + d;
+          *to = __float2bfloat16_rn(__bfloat162float(*to) + v);
         });
         if (lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       } else {
@@ -642,7 +644,6 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
           uint32_t o[32];
           tld<32>(o_tm + 32 * ch, o);
           tld_wait<32>(o);
-          look(o);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             __stcg(reinterpret_cast<uint4*>(slot) + (8 * ch + i) * C::RB + at,
@@ -650,15 +651,11 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         }
         __stcg(slot + C::RB * D + at, m);
         __stcg(slot + C::RB * (D + 1) + at, l);
-        __syncwarp();
-        redo([&](int x, const float* again) {
-          const int row = 128 * rt + (warp & 3) * 32 + x;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const int d = lane * (D / 32) + i;
-            __stcg(slot + ((d >> 2) * C::RB + row) * 4 + (d & 3), again[i] / left_in(TYPE));
-          }
+        left_out([&](int d, float v) {
+          float* to = slot + ((d >> 2) * C::RB + at) * 4 + (d & 3);
+          __stcg(to, __ldcg(to) + v);
         });
+        __syncwarp();
         // each warp joins its own 32 rows: the last CTA's warp to come, in the parts' order
         uint32_t* counter = p.counters + 8 * ca + 4 * rt + (warp & 3);
         __syncwarp();
@@ -838,11 +835,14 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
 #pragma unroll
       for (int s = 0; s < NS; ++s) last_par[s] = -1;
       bool ok = true;
+      uint32_t item = 0;
+      int all_lo, all_hi;
+      all_see<C::RB>(p, wk.cur, all_lo, all_hi);
       while (wk.more()) {
         const Cursor& cur = wk.cur;
         const int t = wk.tile() * KT, tok = t + (pg << shift);
         // a page whose tokens are there and may be seen by some row
-        const bool there = tok < cur.len && tok + ps > cur.lo;
+        const bool there = tok < cur.hi && tok + ps > cur.lo;
         int page = 0;
         if (there)
           page = p.staged ? __ldg(p.staged + cur.seq) + (tok >> shift)
@@ -851,10 +851,10 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         const uint32_t pages = __ballot_sync(0xffffffffu, good) & ((1u << npg) - 1u);
         const bool bad = __any_sync(0xffffffffu, there && !good);
         if (bad && lane == 0) atomicOr(p.error_word, FT_DEVERR_BAD_INDEX);
-        // rows to be cleared: of V whatever no row may see or that holds no token (it meets
-        // probabilities of zero, and must not be NaN), the tokens that share a page with a window's
-        // first one among them; of K those of a bad page
-        const bool clear = kv ? pages != (1u << npg) - 1u || t + KT > cur.len || t < cur.lo : bad;
+        // rows to be cleared: of V whatever no row may see (it meets probabilities of zero, and must
+        // not be NaN), the tokens that share a page with those that some row sees among them; of K
+        // those of a bad page.  Of V, tokens that only some rows see are looked at.
+        const bool clear = kv ? pages != (1u << npg) - 1u || t + KT > min(cur.hi, all_hi) || t < max(cur.lo, all_lo) : bad;
         if (!(ok = wait_all(empty + kv * NS + st, ph ^ 1u))) break;
         const uint32_t dst = ring_addr + st * C::stage;
         const uint32_t fb = bar(full + kv * NS + st), lb = clear ? bar(aux + kv) : fb;
@@ -866,11 +866,31 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         if (clear) {
           if (!(ok = wait_all(aux + kv, aux_ph))) break;
           aux_ph ^= 1u;
-          for (int r = lane; r < KT; r += 32)
-            if (!((pages >> (r >> shift)) & 1u) || t + r >= cur.len || t + r < cur.lo)
-              for (int i = 0; i < 8 * C::panels; ++i)
-                *reinterpret_cast<uint4*>(ring + (kv * NS + st) * C::stage + (i >> 3) * PANEL + r * 128 + (i & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
+          // rows [x0, x1) are as every row of the block sees them, but for pages that are not there
+          bool left_out = false;
+          const int x0 = max(cur.lo, all_lo) - t, x1 = min(cur.hi, all_hi) - t;
+          auto sweep = [&](int ra, int rb) {
+            constexpr int P = 8 * C::panels;  // 16-byte pieces of a row
+#pragma unroll 2
+            for (int u = ra * P + lane; u < rb * P; u += 32) {
+              const int r = u / P, i = u % P, j = t + r;
+              uint4* at = reinterpret_cast<uint4*>(ring + (kv * NS + st) * C::stage + (i >> 3) * PANEL + r * 128 +
+                                                   (((i & 7) ^ (r & 7)) << 4));
+              if (!((pages >> (r >> shift)) & 1u) || j >= cur.hi || j < cur.lo) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else if (kv && (r < x0 || r >= x1)) {
+                uint4 v = *at;
+                if (keep_finite(v)) *at = v, left_out = true;
+              }
+            }
+          };
+          if (bad || x0 >= x1) {
+            sweep(0, KT);
+          } else {
+            sweep(0, min(x0, KT));
+            sweep(max(x1, 0), KT);
+          }
+          if (left_out) note(found, item);
           fence_async();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(fb);
@@ -880,7 +900,10 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
           st = 0;
           ph ^= 1u;
         }
-        wk.next(p);
+        if (wk.next(p)) {
+          ++item;
+          all_see<C::RB>(p, wk.cur, all_lo, all_hi);
+        }
       }
       if (*abort_flag && lane == 0) {  // copies still in flight end before the CTA does
         for (int s = 0; s < NS; ++s)
@@ -901,17 +924,27 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
     const uint8_t* scales = kv ? p.vs : p.ks;
     uint8_t* my_ring = ring + kv * NS * C::stage;
     uint32_t st = 0, ph = 0;
-    ChunkWalk<TYPE, D>* my_walk = reinterpret_cast<ChunkWalk<TYPE, D>*>(walks) + (warp - C::load_warp);
+    uint8_t* mine = walks + 112 * (warp - C::load_warp);
+    ChunkWalk<TYPE, D>* my_walk = reinterpret_cast<ChunkWalk<TYPE, D>*>(mine);
+    int* all = reinterpret_cast<int*>(mine + 96);  // what every row of the item's block sees
+    const int* some = kv ? all : nullptr;
+    uint32_t item = 0;
     Part it;
     auto enter = [&](const ChunkWalk<TYPE, D>& w) {
       it.table = p.page_table + (long long)w.cur.seq * p.table_stride;
-      it.len = w.cur.len;
       it.lo = w.cur.lo;
+      it.hi = w.cur.hi;
       it.head = w.cur.head;
       it.t = w.tile() * KT;
       it.left = w.more() ? (int)(w.end() - w.w) : 0;
+      int all_lo, all_hi;
+      all_see<C::RB>(p, w.cur, all_lo, all_hi);
       __syncwarp();
-      if (lane == 0) *my_walk = w;
+      if (lane == 0) {
+        *my_walk = w;
+        all[0] = all_lo;
+        all[1] = all_hi;
+      }
       __syncwarp();
     };
     // to the next tile; it.left is 0 behind the last one
@@ -921,11 +954,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
         ChunkWalk<TYPE, D> w = *my_walk;
         w.next_item(p);
         enter(w);
+        ++item;
       }
     };
     enter(wk);
     Raw<TYPE, D> x;
-    raw_load<TYPE, D>(p, it, it.t, tile_pages(p, it, it.t, lane), base, scales, lt, x);
+    if (raw_load<TYPE, D>(p, it, it.t, tile_pages(p, it, it.t, lane), base, scales, some, lt, x)) note(found, item);
     next();
     int pages = it.left ? tile_pages(p, it, it.t, lane) : -1;
     for (bool last = false; !last;) {
@@ -933,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D>::threads, 1)
       raw_store<TYPE, D>(my_ring + st * C::stage, lt, x);
       last = it.left == 0;
       if (!last) {
-        raw_load<TYPE, D>(p, it, it.t, pages, base, scales, lt, x);
+        if (raw_load<TYPE, D>(p, it, it.t, pages, base, scales, some, lt, x)) note(found, item);
         next();
         if (it.left) pages = tile_pages(p, it, it.t, lane);
       }

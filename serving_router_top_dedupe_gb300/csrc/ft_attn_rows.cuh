@@ -41,7 +41,7 @@
 // two tiles' latency and the join are nearly all.
 #pragma once
 
-#include "ft_attn_redo.cuh"
+#include "ft_attn_masked.cuh"
 #include "ft_kv_internal.cuh"
 
 namespace ft {
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
   float* q_scale = join_l + kWarps * RB;                      // [RB] scale of a row's scores
   float* row_l = q_scale + RB;                                // [RB] where CTAs join
   int* s_flag = reinterpret_cast<int*>(row_l + RB);
+  int* s_found = s_flag + 1;                                  // values that are not finite were left out of the item
   uint8_t* body = smem + C::qfrag + C::head;
   float* join_o = reinterpret_cast<float*>(body);             // [kWarps][RB][opitch]
 
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       const int rr = cur.rb * RB + r, tok = div_group(p, rr), hd = rr - tok * p.group;
       return p.q + (long long)(cur.q0 + tok) * p.q_stride + (long long)(cur.head * p.group + hd) * D;
     };
+    if (tid == 0) *s_found = 0;
     // the first chunks are on their way while the queries are arranged
     const int n = tb - ta;
     const int32_t* table = p.page_table + (long long)cur.seq * p.table_stride;
@@ -385,9 +387,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         }
       }
     // what every row of the block sees: chunks inside need no mask
-    const int pos0 = cur.len - cur.n + div_group(p, cur.rb * RB);
-    const int pos1 = cur.len - cur.n + div_group(p, cur.rb * RB + rows - 1);
-    const int all_hi = p.causal ? min(cur.len, pos0 + 1) : cur.len, all_lo = p.window > 0 ? max(pos1 - p.window + 1, 0) : 0;
+    int all_lo, all_hi;
+    all_see<RB>(p, cur, all_lo, all_hi);
 
     uint32_t qr[KS][4];
     if (C::q_regs) {
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
       if (!wanted(k)) continue;
       const int t = tok0 + k * UT;
       const uint32_t st = ring + (uint32_t)(k % S) * C::stage;
+      const bool inside = t >= all_lo && t + CHUNK <= all_hi;
       if constexpr (C::q) {
         // The chunk's scale codes as FP32 powers of two (those of the values times 2^lack), zero for
         // tokens that are left out.
@@ -448,6 +450,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
             sc_f[(set * NB + b) * CHUNK + tok] = in ? e8m0(code) * (set ? pow2(C::lack) : 1.f) : 0.f;
           }
         }
+        __syncwarp();
+      }
+      if (!inside && (t < all_lo || min(t + CHUNK, cur.hi) > all_hi)) {  // tokens that only some rows see
+        const int tok = lane % CHUNK, j = t + tok;
+        bool found = false;
+        if (j >= cur.lo && j < cur.hi && (j < all_lo || j >= all_hi)) {
+          constexpr int L = 32 / CHUNK;  // lanes of a token
+          if constexpr (C::q) {
+            for (int b = lane / CHUNK; b < NB; b += L) {
+              float& x = sc_f[(NB + b) * CHUNK + tok];
+              if (x != x) x = 0.f, found = true;
+            }
+          } else {
+            for (int i = lane / CHUNK; i < C::rby / 16; i += L) {
+              uint4* at = reinterpret_cast<uint4*>(ring_g + (k % S) * C::stage + C::kv_bytes + piece<C::rby>(tok, i));
+              uint4 v = *at;
+              if (keep_finite(v)) *at = v, found = true;
+            }
+          }
+        }
+        if (found) *s_found = 1;
         __syncwarp();
       }
       // of a block: this thread's tokens 2c, 2c+1 of column tile nt
@@ -527,7 +550,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         }
       }
       // ------------------------------------------------------------ softmax
-      const bool inside = t >= all_lo && t + CHUNK <= all_hi;
       float mx[MT][2];
       bool move = false;
 #pragma unroll
@@ -688,29 +710,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<TYPE, D, MT>::ctas)) attn_rows_
         acc[i].w += v.w * wt[x];
       }
     }
-    {  // sums that are not finite: because of values that the row does not see?
-      float bad = 0.f;
-#pragma unroll
-      for (int i = 0; i < PC; ++i) bad = fmaf(acc[i].x, 0.f, fmaf(acc[i].y, 0.f, fmaf(acc[i].z, 0.f, fmaf(acc[i].w, 0.f, bad))));
-      uint32_t rows_bad = __ballot_sync(0xffffffffu, bad != bad && r < rows);
-      const int a = max((cur.t0 + ta) * UT, cur.lo), b = min((cur.t0 + tb) * UT, cur.hi);  // the part's tokens
-      while (rows_bad) {
-        const int leader = (__ffs(rows_bad) - 1) / TPR * TPR;  // the row's first thread
-        rows_bad &= ~(((TPR == 32 ? 0u : 1u << TPR) - 1u) << leader);
-        const int row = (warp * 32 + leader) / TPR, pos = cur.len - cur.n + div_group(p, cur.rb * RB + row);
+    if (*s_found) {  // the row's sums are in registers from here on: its first places hold what was left out of them
+      __syncthreads();
+      float* extra = join_o + r * C::opitch;
+      for (int i = sub; i < D; i += TPR) extra[i] = 0.f;
+      __syncwarp();
+      if (r < rows && sub == 0) {
+        const int pos = cur.len - cur.n + div_group(p, cur.rb * RB + r);
         const int see_hi = p.causal ? min(cur.len, pos + 1) : cur.len, see_lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-        if (see_lo <= a && see_hi >= b) continue;
-        float again[D / 32];
-        const float m_row = __shfl_sync(0xffffffffu, mm, leader);
-        if (!redo_row<TYPE, D>(p, cur, cur.rb * RB + row, see_lo, see_hi, a, b, m_row, lane, again)) continue;
-        float* to = join_o + row * C::opitch;  // the row's sums have been taken from here
+        not_finite<TYPE, D>(p, cur, all_lo, all_hi, see_lo, see_hi, (cur.t0 + ta) * UT, (cur.t0 + tb) * UT,
+                            [&](int d, float v) { extra[d] += v; });
+      }
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) to[lane * (D / 32) + i] = again[i];
-        __syncwarp();
-        if (r == row)
-#pragma unroll
-          for (int i = 0; i < PC; ++i) acc[i] = *reinterpret_cast<const float4*>(to + 4 * (sub + TPR * i));
-        __syncwarp();
+      for (int i = 0; i < PC; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(extra + 4 * (sub + TPR * i));
+        acc[i].x += x.x, acc[i].y += x.y, acc[i].z += x.z, acc[i].w += x.w;
       }
     }
     auto put = [&](int row, int piece4, float4 v, float inv) {

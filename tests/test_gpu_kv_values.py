@@ -253,3 +253,80 @@ def test_only_the_counters_of_a_workspace_need_to_be_cleared(F, kind, heads, kv_
         call.out.fill_(77.0)
         assert all(np.array_equal(a, b) for a, b in zip(call.run(), want))
     assert call.word.item() == 0 and call.ws[:F.FT_ATTN_CLEAR_BYTES].max().item() == 0
+
+
+# Batches whose rows see different tokens of their blocks: few rows (one and two row tiles) and many.
+PARTLY = [(4, 2, 64, 6, 300, 0), (8, 1, 128, 4, 300, 0), (16, 2, 256, 3, 300, 0), (4, 2, 64, 20, 300, 7), (8, 1, 128, 9, 300, 5),
+          (4, 1, 64, 200, 500, 0), (8, 1, 128, 100, 500, 0), (16, 2, 256, 70, 400, 0), (1, 1, 128, 300, 700, 0),
+          (64, 2, 64, 600, 1000, 40), (64, 1, 128, 400, 900, 130), (32, 1, 256, 400, 600, 3)]
+
+
+@pytest.mark.parametrize("kind,copies", [(0, True), (1, True), (1, False), (2, True), (2, False)])
+@pytest.mark.parametrize("heads,kv_heads,dim,new,length,window", PARTLY)
+def test_single_elements_that_are_not_finite(F, kind, copies, heads, kv_heads, dim, new, length, window):
+    """Some elements (quantised: 1x32 blocks) of some new tokens' values are infinite or NaN.  Rows that do not see such a
+    token are as if it were not there; rows that do have the sum that IEEE gives in those columns, and the others as always."""
+    rng = np.random.default_rng(new + dim)
+    pages = -(-length // 32)
+    cache = K.Cache(F, kind, kv_heads, dim, 32, pages, 9)
+    table = np.arange(pages, dtype=np.int32)[None]
+    call = X.Call(F, cache, heads, [new], [length], table, window=window, wide=0 if window or new < 30 else WIDE, copies=copies)
+    keep = {0, 1, new // 2, new - 2, new - 1} | set(range(0, new, max(1, new // 23)))
+    clean = cache.value[1].copy()
+    extra = np.zeros_like(clean)                       # what is not finite
+    for j in rng.choice(np.arange(length - new, length), min(new, 9), replace=False):
+        h, col = int(rng.integers(kv_heads)), int(rng.integers(dim))
+        at = (j // 32, h, j % 32)
+        if kind == 0:
+            value = [np.inf, -np.inf, np.nan][int(rng.integers(3))]
+            cache.t[1][at[0], at[1], at[2], col] = value
+            extra[at][col], clean[at][col] = value, 0.0
+        else:
+            block = slice(col // 32 * 32, col // 32 * 32 + 32)
+            cache.scales[1][at[0], at[1], at[2], col // 32] = 255
+            extra[at][block], clean[at][block] = np.nan, 0.0
+    cache.value[1] = clean
+    ref = call.reference(lambda s, i: i in keep)
+    got = call.run()
+    assert call.word.item() == 0
+    bad = np.zeros_like(ref[0])                        # what the rows see of it, summed
+    group = heads // kv_heads
+    for i in keep:
+        p = length - new + i
+        lo = max(0, p - window + 1) if window else 0
+        for h in range(kv_heads):
+            with np.errstate(invalid="ignore"):
+                bad[i, h * group:(h + 1) * group] = extra[:, h].reshape(-1, dim)[lo:p + 1].sum(0)
+    some = np.array([i in keep for i in range(new)])[:, None, None] & (bad != 0)
+    assert some.any()
+    assert np.array_equal(got[0][some], bad[some], equal_nan=True)
+    X.check(np.where(some, ref[0], got[0]), got[1], ref)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_a_long_chunk_whose_last_value_is_not_finite(F, kind):
+    """Every row but the last is as it should be, in about the time that the chunk takes anyway."""
+    heads, kv_heads, dim, length, page = 8, 4, 128, 24576, 64
+    pages = length // page
+    cache = K.Cache(F, kind, kv_heads, dim, page, pages, 2)
+    table = np.random.default_rng(1).permutation(pages).astype(np.int32)[None]
+    call = X.Call(F, cache, heads, [length], [length], table)
+    keep = {5, 4000, length - 100, length - 3, length - 2}
+    ref = call.reference(lambda s, i: i in keep)
+    call.run()
+    took = []
+    for put in (False, True):
+        if put and kind == 0:
+            cache.t[1][table[0, -1], :, page - 1] = float("nan")
+        elif put:
+            cache.scales[1][table[0, -1], :, page - 1] = 255
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        got = call.run()
+        b.record()
+        b.synchronize()
+        took.append(a.elapsed_time(b))
+        assert call.word.item() == 0
+        X.check(*got, ref)
+    assert np.all(np.isnan(got[0][-1])) and np.all(np.isfinite(got[0][:-1])) and np.all(np.isfinite(got[1]))
+    assert took[1] < 5 * took[0] + 10, took
