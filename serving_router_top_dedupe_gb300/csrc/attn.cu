@@ -48,7 +48,7 @@ static_assert(kStageHead == 4352, "the copy's part of the workspace");
 // From this many rows of a head on, a quantised cache's pages are decoded once into a BF16 copy;
 // below it each block of 256 rows decodes what it reads.  Both sides measured (us, decoded where
 // it is read / copied; 16 query heads over 4 cache heads of 128, 16 sequences of 4096 tokens):
-// MXFP8 512 rows 117 / 136, 1024 193 / 183, 2048 332 / 287; MXFP4 105 / 128, 179 / 175, 316 / 277.
+// MXFP8 512 rows 119 / 138, 1024 199 / 189, 2048 343 / 296; MXFP4 109 / 128, 187 / 181, 326 / 285.
 constexpr int kStageRows = 1024;
 
 // Tokens of the cache that a sequence's new ones may see, at most (its length is not known here).
@@ -63,15 +63,15 @@ long long may_see(const AttnParams& p, long long rows) {
 // few-row kernel's rate.  Measured with 16 sequences of 8192 tokens and 4 cache heads (us, few-row
 // kernel / chunk kernel, one launch each):
 //              16 rows      32 rows      48 rows     64 rows    128 rows
-//   BF16  64   44 / 62      62 / 62      79 / 60     97 / 62    156 / 62
-//   BF16 128   66 / 81     107 / 83     142 / 83    177 / 83    302 / 85
-//   BF16 256  100 / 113    178 / 115    251 / 115   326 / 115   603 / 118
-//   MXFP8 64   33 / 76      46 / 76      60 / 76     74 / 76    134 / 76
-//   MXFP8 128  46 / 105     68 / 105     95 / 105   115 / 105   210 / 105
-//   MXFP8 256  87 / 187    136 / 189    187 / 187   237 / 189   440 / 188
-//   MXFP4 64   31 / 74      44 / 72      60 / 72     72 / 72    130 / 72
-//   MXFP4 128  44 / 93      64 / 93      89 / 94    109 / 93    201 / 93
-//   MXFP4 256  72 / 169    120 / 171    165 / 169   212 / 171   398 / 169
+//   BF16  64   44 / 60      62 / 62      79 / 60     97 / 62    158 / 61
+//   BF16 128   67 / 83     109 / 83     146 / 83    181 / 83    319 / 85
+//   BF16 256  101 / 115    180 / 116    250 / 115   329 / 117   616 / 118
+//   MXFP8 64   33 / 81      46 / 81      62 / 81     74 / 81    134 / 81
+//   MXFP8 128  48 / 109     70 / 108     97 / 109   118 / 108   216 / 109
+//   MXFP8 256  81 / 190    128 / 193    177 / 191   226 / 191   421 / 191
+//   MXFP4 64   31 / 74      44 / 74      58 / 74     72 / 74    130 / 74
+//   MXFP4 128  42 / 95      64 / 95      89 / 95    109 / 95    201 / 95
+//   MXFP4 256  72 / 165    120 / 165    165 / 163   212 / 164   398 / 165
 // which is the first rule.  The second: where there is little to do in all, the shorter start
 // decides whatever the rows (one sequence of 4096 tokens, 64 rows: BF16 19 / 33, MXFP8 23 / 51,
 // MXFP4 23 / 48 with heads of 128; BF16 27 / 42 with heads of 256).  The lengths are not known
@@ -87,10 +87,10 @@ bool takes_few(const AttnParams& p, int type, int D, long long rows) {
 // Whether a batch's sequences of few rows (single tokens, mostly) get a launch of the few-row
 // kernel of their own, before the one for the others: sequences of different numbers of new tokens,
 // and much to read.  Measured (us, one launch / two), one chunk besides single tokens that each see
-// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 144 / 99, 4 x 128 117 / 121,
-// 2 x 256 129 / 148; 31 and a chunk of 512 over 2048: MXFP8 339 / 126, 294 / 132, 271 / 152, MXFP4
-// 304 / 123, 267 / 123, 242 / 140; 63 and a chunk of 1024 over 8192: MXFP8 586 / 237, 476 / 274,
-// 587 / 286, BF16 425 / 284, 328 / 316, 263 / 306: over a BF16 cache of 256-wide heads both kernels
+// 8192 tokens: 15 and a chunk of 64, MXFP8, cache heads x head_dim 8 x 64 146 / 103, 4 x 128 120 / 122,
+// 2 x 256 132 / 146; 31 and a chunk of 512 over 2048: MXFP8 342 / 125, 302 / 137, 271 / 152, MXFP4
+// 302 / 124, 273 / 125, 245 / 141; 63 and a chunk of 1024 over 8192: MXFP8 600 / 235, 487 / 280,
+// 596 / 284, BF16 423 / 282, 339 / 320, 263 / 306: over a BF16 cache of 256-wide heads both kernels
 // read a block's tokens at about the same rate, and one launch does.  With little to read the second
 // launch costs more than it saves (7 that see 1000 and a chunk of 1024: 57 / 86).
 constexpr int kFewRows = 16;

@@ -20,10 +20,11 @@
 // about 3500 clocks (84 for an MMA; the rest is between batches of MMAs, whose queue holds three).
 // With 64-wide heads the softmax is as long as the products; with 256-wide ones every CTA's row tile
 // takes all of K and V out of L2, 128 KB a tile and SM, and that bounds it over long caches.
-// Measured: 8192 new tokens, 32 query heads over 4 of 128, BF16: 466 us = 1181 TFLOP/s; 2048 over
-// 65536 (MXFP8, decoded once): 1630-1680 us = 1300; 500 over 100001, heads of 256: 705 us =
-// 1158.  Quantised pages decoded where they are read, 512 rows over 16 x 8192 tokens of 4 x 128:
-// MXFP8 197 us, MXFP4 179, BF16 142: there the decoding warps bound it.
+// Measured, other inputs each time (the same again and again): 8192 new tokens, 32 query heads over 4
+// of 128, BF16: 464 us (462) = 1184 TFLOP/s; 2048 over 65536 (MXFP8, decoded once): 1676 us (1646) =
+// 1292; 500 over 100001, heads of 256: 744 us (700) = 1098.  Quantised pages decoded where they are
+// read, 512 rows over 16 x 8192 tokens of 4 x 128: MXFP8 203 us, MXFP4 181, BF16 144: there the
+// decoding warps bound it.
 //
 // Warps 0-3 (and 4-7): softmax, output.  Then one warp that issues every MMA, and the loaders:
 // two warps of TMA (K, V) for a BF16 cache, eight warps that decode into the same layout for a
@@ -48,7 +49,9 @@ using rows::pack;
 
 constexpr int KT = 128;           // cached tokens of a tile
 constexpr int PANEL = KT * 128;   // bytes of 64 columns of a tile: rows of 128 bytes, 128-byte swizzle
-constexpr float kJoin = 1.2f;     // tiles' time that a part of an item costs the join (0 to 2 measure the same)
+// Tiles' time that a part of an item costs the join: an estimate on which little hangs, as 0 to 2
+// measure the same wherever chunks fill the GPU.
+constexpr float kJoin = 1.2f;
 constexpr float kSlack = 8.f;     // log2 units by which scores may pass the running maximum
 
 template <int TYPE, int D>

@@ -31,13 +31,14 @@
 // are rarely rescaled.
 //
 // Roundings: probabilities (times the scale of quantised values) to BF16 for their product with the
-// values: one rounding of half a unit in the last of 8 bits of each term, what the tensor core takes;
-// everything summed is FP32.
+// values: one rounding of half a unit in the last of 8 bits of each term, what the tensor core takes.
+// Their sum is taken before it, so that it is not off by what rounds in one direction; everything
+// summed is FP32.
 //
 // Measured: 64 single tokens over 16384 tokens each, 4 cache heads of 128, 8 rows of a head: BF16
-// 320 us = 6.7 TB/s, bound by memory; MXFP8 193 us = 5.7 TB/s; MXFP4 193 us = 3.0 TB/s, bound by the
-// decoding: both take the same instructions for a chunk, about 970, and issue one in 52 % of the
-// clocks; 32 rows 315 and 302 us.  One sequence of 4001 tokens: 15 us, of which a launch, the plan,
+// 322 us = 6.7 TB/s, bound by memory; MXFP8 211 us = 5.3 TB/s; MXFP4 199 us = 2.9 TB/s, bound by the
+// decoding: both take about as many instructions for a chunk, 1090 for MXFP8, and issue one in 54 %
+// of the clocks; 32 rows 328 and 317 us.  One sequence of 4001 tokens: 15 us, of which a launch, the plan,
 // two tiles' latency and the join are nearly all.
 #pragma once
 
@@ -162,20 +163,20 @@ struct Cfg {
   static constexpr bool q = TYPE != FT_KV_BF16;
   static constexpr int RB = 16 * MT;  // rows of a block
   // Tokens of a warp's step.  Quantised: twice as many independent products in a chain that is long
-  // for decoding (32 / 16 tokens: MXFP8 8 rows 193 / 217 us, MXFP4 193 / 215 at the size above; 32 rows
-  // 315 / 346 and 302 / 330); 256-wide heads have no registers for that, BF16 has no such chain.
+  // for decoding (32 / 16 tokens: MXFP8 8 rows 211 / 230 us, MXFP4 199 / 224 at the size above; 32 rows
+  // 328 / 355 and 317 / 337); 256-wide heads have no registers for that, BF16 has no such chain.
   static constexpr int CHUNK = q && D <= 128 ? 32 : 16;
   static constexpr int UT = CHUNK * kWarps;          // tokens of a tile
-  // Counts of an item besides its tiles (64 ragged MXFP8 sequences: 0 91 us, 3 55, 8 62).
+  // Counts of an item besides its tiles (64 ragged MXFP8 sequences: 0 92 us, 3 57, 8 65).
   static constexpr int OV = CHUNK == 32 ? 3 : 6;
-  // Tiles' time that a part of an item costs the join (the same 55 us, with 2.0 68; one sequence
-  // of 4001 tokens 15 and 20 us).
+  // Tiles' time that a part of an item costs the join (the same 57 us, with 2.0 72; one sequence
+  // of 4001 tokens 15 and 21 us).
   static constexpr float join_cost = 0.35f;
   static constexpr int rby = row_bytes(TYPE, D), sby = scale_bytes(TYPE, D);
   static constexpr int kv_bytes = CHUNK * rby;
   static constexpr int stage = 2 * kv_bytes + 2 * CHUNK * sby;
   static constexpr int scales = q ? 2 * CHUNK * (D / 32) * 4 : 0;  // a warp's chunk of scales in FP32
-  // per SM, as registers allow (MXFP8, 4 CTAs of 128 registers: 232 us in place of 193)
+  // per SM, as registers allow (MXFP8, 4 CTAs of 128 registers: 341 us in place of 205)
   static constexpr int ctas = D == 256 ? (q ? 2 : 1) : q && MT == 1 ? 3 : 2;
   static constexpr int room = ctas == 1 ? 200 * 1024 : ctas == 2 ? 100 * 1024 : 66 * 1024;
   static constexpr int fit = room / (kWarps * stage);
@@ -848,7 +849,7 @@ cudaError_t launch(const AttnParams& p, int n_sm, cudaStream_t s) {
 }
 
 // rows: of one cache head of a sequence, at most.  Up to 16 rows take one row tile (the second
-// one's products would be for nothing: 193 / 315 us above), more take two, for which a chunk is
+// one's products would be for nothing: 211 / 328 us above), more take two, for which a chunk is
 // decoded once; 256-wide heads have registers for one.
 template <int TYPE>
 cudaError_t launch_type(const AttnParams& p, int D, int rows, int n_sm, cudaStream_t s) {

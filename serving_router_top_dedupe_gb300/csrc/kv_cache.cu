@@ -9,7 +9,9 @@
 // of a 1x32 block find its maximum with two shuffles, and nothing goes through shared memory.
 // Measured: 131072 MXFP8 tokens of 4 x 128 read in 72.5 us (5.6 TB/s); 131072 tokens of 8 x 128 at
 // slots in no order: BF16 written in 192 us (5.6 TB/s), MXFP8 187 (4.3) and read in 171 (4.8), MXFP4
-// 175 (3.9) and 164 (4.1): rows of 64 or 128 bytes fill the memory's bursts less well.
+// 175 (3.9) and 164 (4.1).  Why the quantised ones stay behind has not been found: most of their
+// bytes are the dense BF16 rows, which the BF16 form moves at full rate; one-byte stores and loads of
+// scales, and rows of 64 or 128 bytes in no order, are what they have besides.
 #include <cstdarg>
 #include <cstdio>
 
