@@ -37,7 +37,10 @@ class Layers:
         w = synth.tiny()
         self.w, self.chunk, self.length = w, chunk, 0
         self.banks = synth.ExpertPool(w).routed_banks()
-        self.stream = torch.cuda.current_stream().cuda_stream
+        # Both halves of a layer, and torch's operations between them, go to one stream.  It has to be named: the legacy
+        # default stream is NULL, for which the MoE half would make a stream of its own that nothing here waits for.
+        self.on = torch.cuda.Stream()
+        self.stream = self.on.cuda_stream
         # B_H below B_P: every expert that misses the slot pool is filled, none is left to the host
         cfg = F.make_config(w.n_layers, w.hidden, w.inter, w.n_experts, w.top_k, False, F.FT_W_BF16, 1, 2 * w.n_experts,
                             50.0, 40.0, max_prefill_tokens=chunk, compute_stream=self.stream)
@@ -69,8 +72,16 @@ class Layers:
         self.error = torch.zeros(1, dtype=torch.int32, device="cuda")
 
     def forward(self, x, keep=None):
-        """Hidden states [n][hidden] BF16 of the next n tokens -> theirs after the layers.  keep: a list that gets every
-        layer's (queries, attention output)."""
+        """Hidden states [n][hidden] BF16 of the next n tokens -> theirs after the layers, for the current stream.  keep: a
+        list that gets every layer's (queries, attention output)."""
+        caller = torch.cuda.current_stream()
+        self.on.wait_stream(caller)
+        with torch.cuda.stream(self.on):
+            x = self._forward(x, keep)
+        caller.wait_stream(self.on)
+        return x
+
+    def _forward(self, x, keep):
         n, w = x.shape[0], self.w
         at = torch.arange(self.length, self.length + n, dtype=torch.int32, device="cuda")
         slots = self.table[0, (at // PAGE).long()] * PAGE + at % PAGE

@@ -9,7 +9,8 @@
  * Conventions as in ft_moe.h: a call returns FT_OK or an ft_status (ft_last_error() has the
  * message), argument errors change nothing, work is enqueued on the given stream of the
  * current device (NULL: the legacy default stream) without a host synchronisation, and BF16
- * values are raw 16-bit patterns.
+ * values are raw 16-bit patterns.  A layer's two halves follow one another on one stream: name it
+ * here and in ft_moe_config, where NULL means a stream of the library's own.
  */
 #ifndef FT_KV_H
 #define FT_KV_H
